@@ -82,7 +82,8 @@ enum {
                                        /* (entry -1) or not the first slot of a page (slot % 64 != 0)  */
     MLA_DEVERR_WORKSPACE_STATE = 128,  /* decode: a workspace arrival word was not zero at the call's  */
                                        /* start (workspace not zero-filled before its first use)       */
-    MLA_DEVERR_SLOT_OUT_OF_RANGE = 256 /* KV write: cache_loc[i] not a pool row: that token skipped    */
+    MLA_DEVERR_SLOT_OUT_OF_RANGE = 256,/* KV write: cache_loc[i] not a pool row: that token skipped    */
+    MLA_DEVERR_NO_FREE_PAGE = 512      /* chunk metadata: the free list is too short: entry and slot -1 */
 };
 
 typedef struct CUstream_st* mla_stream_t;  /* identical to cudaStream_t */
@@ -358,6 +359,98 @@ MLA_API mla_status_t mla_extend_paged_prefix(const void* q, int32_t bs, int32_t 
                                              float softmax_scale, const float* descale_k, int32_t sm_count,
                                              void* out, float* lse, void* workspace, size_t workspace_bytes,
                                              mla_stream_t stream);
+
+/*
+ * Metadata of a ragged batch, in one launch: request b has prefix_lens[b] cached tokens and brings
+ * chunk_lens[b] new ones (any number, 0 included), whose rows follow one another without gaps.  The
+ * counterpart of mla_build_decode_metadata (flashmla_backend.py, init_forward_metadata) for
+ * new-token counts that differ, together with the slots of the new tokens (the page's
+ * forward_batch.out_cache_loc, which set_kv_buffer takes).  With p_b, n_b, L_b = p_b + n_b:
+ *   cache_seqlens  int32 [bs]: L_b
+ *   cu_seqlens     int32 [bs + 1]: cu[b] = n_0 + .. + n_{b-1}
+ *   block_table    int32 [bs, block_table_stride], as mla_build_block_table writes it for L_b:
+ *                  entry p < cdiv(L_b, 64) is the page of positions 64 p .., the entries behind, up
+ *                  to max_pages, are -1 when fill_tail != 0 and untouched otherwise
+ *   positions      int32 [num_tokens]: token cu[b] + i has position p_b + i
+ *   cache_loc      int32 [num_tokens]: its pool slot 64 * page + position % 64
+ *   chunk_plan     int32 [num_parts, 8], 16-byte aligned: the split plan of mla_chunk_paged for
+ *                  num_heads query heads and `causal` (row = begin request, row tile, key tile, end
+ *                  request, row tile, key tile, 0, 0; the end exclusive)
+ *   pages_taken    int32 [1], may be NULL: new pages taken from free_pages
+ * Entries of positions / cache_loc behind the last request's (cu[bs] .. num_tokens - 1, a padded
+ * batch) get 0 / pad_slot when fill_tail != 0 and are untouched otherwise.
+ *
+ * Slots.  free_pages == NULL: every new token's slot is in req_to_token already and is read from
+ * there.  Otherwise new pages come from free_pages: request b takes the next
+ * cdiv(L_b, 64) - cdiv(p_b, 64) of them in request order, a page already begun is filled up first,
+ * and the new tokens' slots are entered into req_to_token.  The caller drops the first *pages_taken
+ * pages from its list.  The requests' rows must differ then (two requests of one row would enter
+ * their slots at the same places).
+ *
+ *   req_to_token   int32 [req_to_token_rows, req_to_token_stride]
+ *   req_pool_indices [bs] and free_pages [num_free_pages] of index_dtype (int32 or int64)
+ *   prefix_lens, chunk_lens [bs] of lens_dtype (int32 or int64); negative ones count as 0
+ *   num_tokens     rows of the batch: at least cu[bs] (what goes beyond is cut off and reported)
+ *   num_parts      mla_num_chunk_parts(sm_count); at most 1024
+ *   page_size      must be 64
+ * bs at most 4096 and num_tokens * num_heads below 2^31 - 256, else MLA_ERR_UNSUPPORTED.  bs == 0
+ * is allowed (cu_seqlens[0] = 0, an empty plan).  Device checks: a row outside req_to_token leaves
+ * the request without pages and slots (-1; MLA_DEVERR_ROW_OUT_OF_RANGE); positions past max_pages
+ * pages or past the row of req_to_token get slot -1 (MLA_DEVERR_LEN_OUT_OF_RANGE); a slot of
+ * req_to_token that is negative, or not page-aligned where a page begins, sets
+ * MLA_DEVERR_SLOT_INVALID; a free list that is too short gives page and slot -1 and sets
+ * MLA_DEVERR_NO_FREE_PAGE.
+ */
+MLA_API mla_status_t mla_build_chunk_metadata(
+    int32_t* req_to_token, int64_t req_to_token_rows, int64_t req_to_token_stride, const void* req_pool_indices,
+    int32_t index_dtype, const void* prefix_lens, const void* chunk_lens, int32_t lens_dtype, int32_t bs,
+    int32_t num_tokens, const void* free_pages, int64_t num_free_pages, int32_t num_heads, int32_t causal,
+    int32_t num_parts, int32_t* block_table, int64_t block_table_stride, int32_t max_pages, int32_t page_size,
+    int32_t fill_tail, int32_t pad_slot, int32_t* cache_seqlens, int32_t* cu_seqlens, int32_t* positions,
+    int32_t* cache_loc, int32_t* chunk_plan, int32_t* pages_taken, mla_stream_t stream);
+
+/* Parts of a chunk_plan: one per pair of SMs.  Returns -1 on a non-positive argument.  Pure host. */
+MLA_API int32_t mla_num_chunk_parts(int32_t sm_count);
+
+/*
+ * Bytes of workspace mla_chunk_paged needs: two fp32 partial results of 128 rows per part, whatever
+ * the batch.  Needs no initialisation.  Pure host function; 0 on a num_parts outside [1, 1024].
+ */
+MLA_API size_t mla_chunk_workspace_bytes(int32_t num_parts);
+
+/*
+ * Paged MLA attention of ragged chunks: mla_decode_paged for new-token counts that differ
+ * (flashmla_backend.py, forward_extend, for chunked prefill, prompts, single tokens or a mix).
+ * The new tokens' rows are in the cache already (mla_set_kv_buffer), as their requests' last ones.
+ *
+ * For every request b, its token i < n = cu_seqlens[b + 1] - cu_seqlens[b] (row cu_seqlens[b] + i
+ * of q, out and lse) and head h:
+ *   L = cache_seqlens[b]; keys j < lim with lim = L - n + i + 1 when causal and lim = L otherwise;
+ *   k_j, v_j, s_j, lse, o and the arithmetic as for mla_decode_paged.
+ *   A row with no allowed key gets o = 0 and lse = -inf.  Rows of no request (behind the last one)
+ *   are left as they were.
+ *
+ *   q              bf16 [num_tokens, h_q, head_dim], contiguous (e4m3 q: MLA_ERR_UNSUPPORTED)
+ *   head_dim, head_dim_v, k_cache .. max_pages, softmax_scale, descale_q, descale_k  as for
+ *                  mla_decode_paged.  Rows of a page at or past L may hold anything (infinities and
+ *                  NaN too); the rows below L must be finite
+ *   cu_seqlens     int32 [bs + 1], non-decreasing, within [0, num_tokens] (other values are clamped)
+ *   chunk_plan, num_parts  from mla_build_chunk_metadata for the same lengths, h_q and causal
+ *   out, lse       bf16 [num_tokens, h_q, 512], fp32 [num_tokens, h_q] (written)
+ *   workspace      at least mla_chunk_workspace_bytes(num_parts) bytes, 256-byte aligned; calls that
+ *                  overlap on the GPU need one each
+ * num_tokens * h_q below 2^31 - 256, else MLA_ERR_UNSUPPORTED.  The result does not depend on how
+ * calls are timed: pieces of a cut unit are summed in the plan's order.  Errors and device checks
+ * are those of mla_decode_paged.
+ */
+MLA_API mla_status_t mla_chunk_paged(const void* q, int32_t q_dtype, int32_t num_tokens, int32_t h_q,
+                                     int32_t head_dim, int32_t head_dim_v, const void* k_cache, int32_t kv_dtype,
+                                     int64_t num_pages, int32_t page_size, const int32_t* block_table,
+                                     int64_t block_table_stride, int32_t max_pages, const int32_t* cache_seqlens,
+                                     const int32_t* cu_seqlens, int32_t bs, const int32_t* chunk_plan,
+                                     int32_t num_parts, float softmax_scale, int32_t causal, const float* descale_q,
+                                     const float* descale_k, void* out, float* lse, void* workspace,
+                                     size_t workspace_bytes, mla_stream_t stream);
 
 /*
  * Test hooks for the failure path of mla_decode_paged; not for production use.  They set

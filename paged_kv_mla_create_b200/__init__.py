@@ -29,7 +29,8 @@ from . import build as _build
 
 __all__ = [
     "build_block_table", "get_mla_metadata", "build_decode_metadata", "mla_decode_paged",
-    "flash_mla_with_kvcache", "set_kv_buffer",
+    "flash_mla_with_kvcache", "set_kv_buffer", "build_chunk_metadata", "mla_chunk_paged",
+    "num_chunk_parts", "chunk_workspace_bytes",
     "num_sm_parts", "workspace_bytes", "read_device_error", "library", "MlaError",
 ]
 
@@ -90,6 +91,16 @@ def library() -> ctypes.CDLL:
     lib.mla_extend_paged_prefix.argtypes = [P, I32, I32, I32, P, P, I32, I64, P, I64, I64, P, I32, P, I32,
                                             ctypes.c_float, P, I32, P, P, P, ctypes.c_size_t, P]
     lib.mla_extend_paged_prefix.restype = I32
+    lib.mla_build_chunk_metadata.argtypes = [P, I64, I64, P, I32, P, P, I32, I32, I32, P, I64, I32, I32, I32, P, I64, I32,
+                                             I32, I32, I32, P, P, P, P, P, P, P]
+    lib.mla_build_chunk_metadata.restype = I32
+    lib.mla_num_chunk_parts.argtypes = [I32]
+    lib.mla_num_chunk_parts.restype = I32
+    lib.mla_chunk_workspace_bytes.argtypes = [I32]
+    lib.mla_chunk_workspace_bytes.restype = SZ
+    lib.mla_chunk_paged.argtypes = [P, I32, I32, I32, I32, I32, P, I32, I64, I32, P, I64, I32, P, P, I32, P, I32, F, I32,
+                                    P, P, P, P, P, SZ, P]
+    lib.mla_chunk_paged.restype = I32
     lib.mla_set_test_hooks.argtypes = [ctypes.c_uint64, I32, I32]
     lib.mla_set_test_hooks.restype = I32
     lib.mla_read_device_error.argtypes = [ctypes.POINTER(I32), P]
@@ -394,6 +405,146 @@ def extend_paged_prefix(q: torch.Tensor, k_new: torch.Tensor, k_cache: torch.Ten
         req_to_token.stride(0), _ptr(rpi), _index_dtype(rpi), _ptr(pl), int(max_prefix_pages),
         float(softmax_scale), _ptr(descale_k), sm_count(dev), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
         _stream(dev)), "mla_extend_paged_prefix")
+    return out, lse
+
+
+def num_chunk_parts(sm_count_: Optional[int] = None) -> int:
+    """Rows of a chunk plan (build_chunk_metadata): one per pair of SMs."""
+    n = library().mla_num_chunk_parts(sm_count_ if sm_count_ is not None else sm_count())
+    if n < 1:
+        raise ValueError("invalid argument to num_chunk_parts")
+    return n
+
+
+def chunk_workspace_bytes(parts: int) -> int:
+    """Bytes of the ragged attention's workspace for a plan of `parts` rows (no initialisation needed)."""
+    n = int(library().mla_chunk_workspace_bytes(int(parts)))
+    if n == 0:
+        raise ValueError("a chunk plan has between 1 and 1024 parts")
+    return n
+
+
+def _int32_vector(t: torch.Tensor, name: str, least: int) -> None:
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < least:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of at least {least} elements")
+
+
+def build_chunk_metadata(req_to_token: torch.Tensor, req_pool_indices: torch.Tensor, prefix_lens: torch.Tensor,
+                         chunk_lens: torch.Tensor, num_tokens: int, max_seqlen_pad: int, num_heads: int,
+                         free_pages: Optional[torch.Tensor] = None, causal: bool = True, pad_slot: int = -1,
+                         fill_tail: bool = True, num_parts: Optional[int] = None,
+                         out: Optional[Tuple[torch.Tensor, ...]] = None):
+    """Metadata of a ragged batch in one launch: request b has prefix_lens[b] cached tokens and
+    brings chunk_lens[b] new ones, their rows one request after another in num_tokens rows.
+    Returns (block_table int32 [bs, max_seqlen_pad], cache_seqlens int32 [bs], cu_seqlens int32
+    [bs + 1], positions int32 [num_tokens], cache_loc int32 [num_tokens], chunk_plan int32 [parts, 8],
+    pages_taken int32 [1], or None without free_pages).
+
+    Without free_pages the new tokens' slots are read from req_to_token; with them new pages are
+    taken from the list, in request order, and the new slots entered into req_to_token (the
+    requests' rows must differ then).  Rows behind the last request get position 0 and slot
+    pad_slot when fill_tail (-1: not a slot; set_kv_buffer skips and reports it), else nothing."""
+    _require_cuda(req_to_token, req_pool_indices, prefix_lens, chunk_lens, free_pages)
+    if req_to_token.dtype != torch.int32 or req_to_token.dim() != 2 or req_to_token.stride(1) != 1:
+        raise ValueError("req_to_token must be a row-major int32 matrix")
+    if num_tokens < 0 or max_seqlen_pad < 0 or num_heads <= 0:
+        raise ValueError("num_tokens and max_seqlen_pad must not be negative, num_heads must be positive")
+    bs = int(req_pool_indices.shape[0])
+    for name, t in (("req_pool_indices", req_pool_indices), ("prefix_lens", prefix_lens), ("chunk_lens", chunk_lens)):
+        if t.dim() != 1 or t.shape[0] != bs:
+            raise ValueError(f"{name} must be a vector of one entry per request")
+    if prefix_lens.dtype != chunk_lens.dtype:
+        raise ValueError("prefix_lens and chunk_lens must have the same dtype")
+    dev = req_to_token.device
+    rpi, pl, cl = req_pool_indices.contiguous(), prefix_lens.contiguous(), chunk_lens.contiguous()
+    if free_pages is not None:
+        if free_pages.dim() != 1 or free_pages.dtype != rpi.dtype:
+            raise ValueError("free_pages must be a vector of req_pool_indices' dtype")
+        free_pages = free_pages.contiguous()
+    for t in (rpi, pl, cl, free_pages, *(out or ())):
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors must be on the same device")
+    with torch.cuda.device(dev):
+        parts = int(num_parts) if num_parts is not None else num_chunk_parts(sm_count(dev))
+        if out is None:
+            new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)
+            out = (new(bs, max_seqlen_pad), new(bs), new(bs + 1), new(num_tokens), new(num_tokens), new(parts, 8),
+                   new(1) if free_pages is not None else None)
+        bt, seqlens, cu, positions, loc, plan, taken = out
+        if bt.dtype != torch.int32 or bt.dim() != 2 or bt.stride(1) != 1 or bt.shape[0] < bs or bt.shape[1] < max_seqlen_pad:
+            raise ValueError("block_table must be a row-major int32 [bs, max_seqlen_pad] matrix")
+        _int32_vector(seqlens, "cache_seqlens", bs)
+        _int32_vector(cu, "cu_seqlens", bs + 1)
+        _int32_vector(positions, "positions", num_tokens)
+        _int32_vector(loc, "cache_loc", num_tokens)
+        _int32_vector(plan, "chunk_plan", 8 * parts)
+        if taken is not None:
+            _int32_vector(taken, "pages_taken", 1)
+        # a free list without entries is still a list (its data pointer may be null)
+        free_ptr = None if free_pages is None else ctypes.c_void_p(free_pages.data_ptr() or rpi.data_ptr())
+        _check(library().mla_build_chunk_metadata(
+            _ptr(req_to_token), req_to_token.shape[0], req_to_token.stride(0), _ptr(rpi), _index_dtype(rpi), _ptr(pl),
+            _ptr(cl), _index_dtype(pl), bs, int(num_tokens), free_ptr, free_pages.numel() if free_pages is not None else 0,
+            int(num_heads), int(bool(causal)), parts, _ptr(bt), bt.stride(0), int(max_seqlen_pad), PAGE_SIZE,
+            int(bool(fill_tail)), int(pad_slot), _ptr(seqlens), _ptr(cu), _ptr(positions), _ptr(loc), _ptr(plan),
+            _ptr(taken), _stream(dev)), "mla_build_chunk_metadata")
+    return out
+
+
+def mla_chunk_paged(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor, cache_seqlens: torch.Tensor,
+                    cu_seqlens: torch.Tensor, head_dim_v: int, chunk_plan: torch.Tensor, softmax_scale: float,
+                    causal: bool = True, descale_q: Optional[torch.Tensor] = None,
+                    descale_k: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Paged MLA attention of ragged chunks: rows [cu_seqlens[b], cu_seqlens[b + 1]) of q (bf16
+    [num_tokens, h_q, 576]) are request b's new tokens, the last of its cache_seqlens[b] cached rows;
+    each sees the rows up to its own (causal) or all of them.  Lengths, offsets and plan as
+    build_chunk_metadata gives them for h_q heads and the same causal; k_cache bf16, float8_e4m3fn or
+    float8_e5m2.  Returns (o bf16 [num_tokens, h_q, 512], lse fp32 [num_tokens, h_q]); rows of no
+    request keep what out / lse held."""
+    _require_cuda(q, k_cache, block_table, cache_seqlens, cu_seqlens, chunk_plan, descale_q, descale_k, out, lse, workspace)
+    if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 [num_tokens, h_q, head_dim] tensor")
+    num_tokens, h_q, head_dim = (int(x) for x in q.shape)
+    if not k_cache.is_contiguous() or k_cache.shape[-1] != head_dim:
+        raise ValueError("k_cache must be contiguous with head_dim-wide rows")
+    if k_cache.numel() % (PAGE_SIZE * head_dim):
+        raise ValueError("k_cache must hold whole 64-token pages")
+    if k_cache.dtype not in _CACHE_DTYPES:
+        raise ValueError(f"unsupported k_cache dtype {k_cache.dtype}")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.stride(1) != 1:
+        raise ValueError("block_table must be a row-major int32 [bs, max_pages] matrix")
+    bs = int(block_table.shape[0])
+    _int32_vector(cache_seqlens, "cache_seqlens", bs)
+    _int32_vector(cu_seqlens, "cu_seqlens", bs + 1)
+    if chunk_plan.dtype != torch.int32 or chunk_plan.dim() != 2 or chunk_plan.shape[1] != 8 or not chunk_plan.is_contiguous():
+        raise ValueError("chunk_plan must be a contiguous int32 [parts, 8] matrix")
+    for name, d in (("descale_q", descale_q), ("descale_k", descale_k)):
+        if d is not None and (d.dtype != torch.float32 or d.numel() < 1):
+            raise ValueError(f"{name} must be a float32 tensor of one element")
+    dev = q.device
+    for t in (k_cache, block_table, cache_seqlens, cu_seqlens, chunk_plan, descale_q, descale_k, out, lse, workspace):
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors must be on the same device")
+    if out is not None and (out.dtype != torch.bfloat16 or not out.is_contiguous()
+                            or tuple(out.shape) != (num_tokens, h_q, head_dim_v)):
+        raise ValueError("out must be a contiguous bf16 [num_tokens, h_q, head_dim_v] tensor")
+    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or tuple(lse.shape) != (num_tokens, h_q)):
+        raise ValueError("lse must be a contiguous float32 [num_tokens, h_q] tensor")
+    parts = int(chunk_plan.shape[0])
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((num_tokens, h_q, head_dim_v), dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty((num_tokens, h_q), dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty((chunk_workspace_bytes(parts),), dtype=torch.uint8, device=dev)
+        _check(library().mla_chunk_paged(
+            _ptr(q), DTYPE_BF16, num_tokens, h_q, head_dim, int(head_dim_v), _ptr(k_cache), _CACHE_DTYPES[k_cache.dtype],
+            k_cache.numel() // (PAGE_SIZE * head_dim), PAGE_SIZE, _ptr(block_table), block_table.stride(0),
+            int(block_table.shape[1]), _ptr(cache_seqlens), _ptr(cu_seqlens), bs, _ptr(chunk_plan), parts,
+            float(softmax_scale), int(bool(causal)), _ptr(descale_q), _ptr(descale_k), _ptr(out), _ptr(lse),
+            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(dev)), "mla_chunk_paged")
     return out, lse
 
 

@@ -1,0 +1,969 @@
+// Attention of ragged chunks of new tokens over the paged MLA cache for sm_100a: the queries of
+// request b are rows [cu_seqlens[b], cu_seqlens[b + 1]) of q, any number of them (none, one, a
+// prefill chunk, a whole prompt), and token i of n sees the keys j < L - n + i + 1 of the request's
+// L cached rows (causal, its own row last), in the role of flash_mla_with_kvcache in the SGLang
+// FlashMLA backend page (flashmla_backend.py, forward_extend) for new-token counts that differ.
+//
+// A unit is a tile of 128 query rows of one request (row = token * h + head, so one token of 128
+// heads, or eight of 16): the rows share their keys, S = Q K^T and O = P V are dense contractions.
+// One 2-CTA cluster per plan part walks the part's units (chunk_plan.cuh), computing with pair
+// MMAs as the decode kernel does (decode.cuh describes the pair's layout: S split by tokens, O by
+// output columns, the partner's V loaded into the chunks that S no longer needs).  With hundreds of
+// units per part the tensor pipe bounds it (a tile of 128 keys takes ~2,170 cycles of MMAs); with
+// one token per request the cache is read once and HBM does.
+//
+//   * A unit that lies whole in its part writes bf16 o and lse.  A part's first unit may continue
+//     one that the part before began, its last may go on in the next: such pieces store fp32
+//     partials in slot 2 part (continued) or 2 part + 1 (begun here), and chunk_merge_kernel joins
+//     them.  At most two pieces per part, so the workspace does not grow with the batch, and no
+//     piece waits for another.
+//   * Rows of a page at or past L (never written) are cleared in shared memory before P V reads
+//     them: P is 0 there, but 0 x NaN is not.
+#pragma once
+#include "chunk_plan.cuh"
+#include "decode.cuh"
+
+namespace mla {
+namespace chunk {
+
+using decode::kBox;
+using decode::kChunk8;
+using decode::kChunks;
+using decode::kCtaRows;
+using decode::kDqk;
+using decode::kDv;
+using decode::kIdescPV;
+using decode::kIdescPV16;
+using decode::kIdescQK;
+using decode::kIdescQK16;
+using decode::kKSlotBytes;
+using decode::kKSlots;
+using decode::kPage;
+using decode::kPage8Bytes;
+using decode::kPBytes;
+using decode::kQHiBytes;
+using decode::kQHiChunks;
+using decode::kQLoChunks;
+using decode::kQWarp0;
+using decode::kRaw8Off;
+using decode::kRescaleThreshold;
+using decode::kSoftmaxWarp0;
+using decode::kThreads;
+using decode::kTmemCols;
+using decode::kTmemO;
+using decode::kTmemQ;
+using decode::kTmemS;
+using decode::PageWindow;
+
+// Shared-memory map (offsets from the 1024-aligned base).
+constexpr int kOffQ = 0;                            // Q chunks 4..8
+constexpr int kOffK = kOffQ + kQHiBytes;
+constexpr int kOffP = kOffK + kKSlots * kKSlotBytes;
+constexpr int kOffX = kOffP + kPBytes;              // row-max exchange: 2 x 128 floats, row sums 128
+constexpr int kOffStage = kOffX + 2048;             // epilogue staging: 4 warps x 32 rows x 128 B
+constexpr int kOffPSig = kOffStage + 4 * 32 * 128;  // leader: landing words of the peer's signals
+constexpr int kOffBar = kOffPSig + 128;             // words: P 0..3, V 4..7, K 8, Q 9..12, S 16..19, O 20..23
+
+enum : int {
+    kBarKFull = 0,                      // leader (x slots): both CTAs' pages of the tile landed
+    kBarKEmpty = kBarKFull + kKSlots,   // both: the tile's PV finished (slot reusable)
+    kBarQKDone = kBarKEmpty + kKSlots,  // both: the tile's S MMAs finished reading the slot
+    kBarVFull = kBarQKDone + kKSlots,   // leader: the pair's partner V landed
+    kBarQFull = kBarVFull + kKSlots,    // leader: Q landed / was written
+    kBarQEmpty,                         // both: the unit's last S MMA finished (Q reusable)
+    kBarSFull,                          // both (x2): S tile in tensor memory
+    kBarSFree = kBarSFull + 2,          // leader (x2): 8 softmax warps have read S
+    kBarPFull = kBarSFree + 2,          // leader: 8 softmax warps wrote P
+    kBarPvDone,                         // both: the PV MMAs of a tile finished (P reusable)
+    kBarOFull,                          // both: the unit's last PV finished
+    kBarOEmpty,                         // leader: 8 softmax warps read O out
+    kBarXchg,                           // local (x2): the 128 softmax threads posted row maxima
+    kBarLx = kBarXchg + 2,              // local: the 128 softmax threads posted row sums
+    kBarVTail,                          // local: the partner V of a tile with a cut page landed
+    kBarKRaw,                           // local (x2), 8-bit cache: this CTA's page landed
+    kNumBars = kBarKRaw + kKSlots
+};
+constexpr int kOffMisc = kOffBar + kNumBars * 8;    // tensor-memory base, abort flag
+constexpr int kSmemBytes = kOffMisc + 64 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+static_assert(kOffK % 1024 == 0 && kOffP % 1024 == 0 && kOffStage % 1024 == 0,
+              "128-byte swizzle atoms need 1 KB alignment");
+static_assert(kOffBar % 8 == 0, "mbarriers are 8 bytes");
+
+// Partial results, two slots per part: fp32 rows [2 parts, 128, 512] and their lse [2 parts, 128].
+__host__ __device__ constexpr size_t part_o_floats(int parts) { return (size_t)parts * 2 * kTileRows * kDv; }
+
+struct Params {
+    const __nv_bfloat16* q;        // [num_tokens * h, 576]
+    const uint8_t* kv;             // [num_pages * 64, 576]
+    const int32_t* block_table;    // [bs, bt_stride]
+    int64_t bt_stride;
+    int32_t max_pages;
+    const int32_t* cache_seqlens;  // [bs]
+    const int32_t* cu;             // [bs + 1]
+    const int32_t* plan;           // [parts, 8]
+    int32_t bs, h, num_tokens, parts;
+    int64_t num_pages;
+    float scale_log2;              // softmax_scale * log2(e)
+    const float* descale_q;        // nullable
+    const float* descale_k;        // nullable
+    int32_t causal;
+    __nv_bfloat16* out;            // [num_tokens * h, 512]
+    float* lse;                    // [num_tokens * h]
+    float* part_o;                 // [2 parts, 128, 512]
+    float* part_lse;               // [2 parts, 128]
+    uint64_t wait_budget_ns;       // budget of one pipeline wait
+    int32_t withhold_tile;         // test hook: the leader's K load of this tile is not issued (-1: none)
+};
+
+// A unit, or the piece of it that lies in this part: request b, query rows row0 + [0, nrows) of q,
+// key tiles [t0, t1), pages [2 t0, kb1); slot: where the piece's partial goes (-1: the whole unit).
+struct Unit {
+    int b, tok0, row_in_req, nrows, n, L, t0, t1, kb1, slot;
+    int row0;   // first row in q / out
+    __device__ int tiles() const { return t1 - t0; }
+};
+
+// Rows [c0, c1) of request b, whatever the caller's offsets hold.
+__device__ __forceinline__ void request_rows(const int32_t* cu, int b, int num_tokens, int& c0, int& n) {
+    c0 = cu[b];
+    int c1 = cu[b + 1];
+    c0 = c0 < 0 ? 0 : (c0 > num_tokens ? num_tokens : c0);
+    c1 = c1 < c0 ? c0 : (c1 > num_tokens ? num_tokens : c1);
+    n = c1 - c0;
+}
+
+// The units of a part, identical in every role.
+struct UnitIter {
+    int b, m, t, b1, m1, t1;
+    int part;
+    __device__ bool next(const Params& p, Unit& u) {
+        while (b < p.bs && (b < b1 || (b == b1 && (m < m1 || (m == m1 && t < t1))))) {
+            int c0, n;
+            request_rows(p.cu, b, p.num_tokens, c0, n);
+            const int rows = n * p.h;
+            if (m >= (rows + kTileRows - 1) / kTileRows) {
+                ++b;
+                m = t = 0;
+                continue;
+            }
+            const int L = p.cache_seqlens[b];
+            int64_t keys = unit_keys(L, n, p.h, m, p.causal);
+            if (keys > (int64_t)p.max_pages * kPage) keys = (int64_t)p.max_pages * kPage;
+            const int tiles = (int)((keys + kTileKeys - 1) / kTileKeys);
+            const int hi = (b == b1 && m == m1) ? min(t1, tiles) : tiles;
+            const int lo = t;
+            u.b = b;
+            u.tok0 = c0;
+            u.n = n;
+            u.L = L;
+            u.row_in_req = m * kTileRows;
+            u.nrows = min(kTileRows, rows - m * kTileRows);
+            u.row0 = c0 * p.h + m * kTileRows;
+            u.t0 = lo;
+            u.t1 = hi;
+            u.kb1 = min(2 * hi, (int)((keys + kPage - 1) / kPage));
+            u.slot = lo > 0 ? 2 * part : (hi < tiles ? 2 * part + 1 : -1);
+            ++m;
+            t = 0;
+            if (lo >= hi && lo > 0) continue;   // nothing left of a unit whose keys end before the cut
+            return true;
+        }
+        return false;
+    }
+};
+
+__device__ __forceinline__ UnitIter make_iter(const Params& p, int part, bool& ok) {
+    const int4 r0 = *reinterpret_cast<const int4*>(p.plan + 8 * (int64_t)part);
+    const int2 r1 = *reinterpret_cast<const int2*>(p.plan + 8 * (int64_t)part + 4);
+    UnitIter it;
+    it.b = r0.x;
+    it.m = r0.y;
+    it.t = r0.z;
+    it.b1 = r0.w;
+    it.m1 = r1.x;
+    it.t1 = r1.y;
+    it.part = part;
+    ok = it.b >= 0 && it.b <= it.b1 && it.b1 <= p.bs && it.m >= 0 && it.t >= 0 && it.m1 >= 0 && it.t1 >= 0;
+    if (!ok) it.b = p.bs;   // no units
+    return it;
+}
+
+// Widen one 8-bit chunk as decode::widen_chunk_fp8 does, rows at or past `valid` as zeros.
+template <bool kE5M2>
+__device__ __forceinline__ void widen_chunk_rows(uint32_t src, uint32_t dst, int lane, int valid) {
+    uint4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        v[j] = ld_shared_v4u(src + 16u * (uint32_t)(lane + 32 * j));
+        if (((lane + 32 * j) >> 2) >= valid) v[j] = make_uint4(0, 0, 0, 0);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int x = lane + 32 * j;        // row x / 4, 16-value quarter x % 4
+        const uint32_t t = (uint32_t)(x >> 2), q = (uint32_t)(x & 3);
+        const uint32_t row = dst + 128u * t;
+        st_shared_v4u(row + 16u * ((2u * q) ^ (t & 7u)), fp8x2_to_f16x2<kE5M2>(v[j].x), fp8x2_to_f16x2<kE5M2>(v[j].x >> 16),
+                      fp8x2_to_f16x2<kE5M2>(v[j].y), fp8x2_to_f16x2<kE5M2>(v[j].y >> 16));
+        st_shared_v4u(row + 16u * ((2u * q + 1u) ^ (t & 7u)), fp8x2_to_f16x2<kE5M2>(v[j].z),
+                      fp8x2_to_f16x2<kE5M2>(v[j].z >> 16), fp8x2_to_f16x2<kE5M2>(v[j].w), fp8x2_to_f16x2<kE5M2>(v[j].w >> 16));
+    }
+    __syncwarp();
+}
+
+// Clear rows [valid, 64) of the four V chunks at slot positions 4n + c, + 1 (n = 0, 1).
+__device__ __forceinline__ void clear_v_rows(uint32_t slot, int c, int valid, int lane) {
+    if (valid < 0) valid = 0;
+    for (int x = lane; x < (kPage - valid) * 32; x += 32) {
+        const int row = valid + (x >> 5), k = x & 31;   // chunk k / 8, 16-byte unit k % 8
+        const int pos = 4 * (k >> 4) + c + ((k >> 3) & 1);
+        st_shared_v4u(slot + (uint32_t)(pos * kBox + row * 128 + 16 * (k & 7)), 0u, 0u, 0u, 0u);
+    }
+}
+
+// kKv: the cache's element type, 0 bf16, 1 e4m3, 2 e5m2 (8-bit caches are widened to f16).
+template <int kKv>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                 const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap o_map,
+                 const __grid_constant__ CUtensorMap ps_map, const __grid_constant__ Params p) {
+    constexpr bool kFp8 = kKv != 0;
+    constexpr bool kE5M2 = kKv == 2;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * i; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);   // warp-uniform to the compiler
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int part = blockIdx.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kKSlots; ++s) {
+            mbar_init(bar(kBarKFull + s), 1);
+            mbar_init(bar(kBarKEmpty + s), 1);
+            mbar_init(bar(kBarQKDone + s), 1);
+            mbar_init(bar(kBarVFull + s), kFp8 ? 4 : 1);
+            mbar_init(bar(kBarKRaw + s), 1);
+        }
+        // the Q TMA (bf16 cache) and the 4 warps that write Q
+        mbar_init(bar(kBarQFull), (kFp8 ? 0 : 1) + 4);
+        mbar_init(bar(kBarQEmpty), 1);
+        for (int j = 0; j < 2; ++j) {
+            mbar_init(bar(kBarSFull + j), 1);
+            mbar_init(bar(kBarSFree + j), 4);
+        }
+        mbar_init(bar(kBarPFull), 4);
+        mbar_init(bar(kBarPvDone), 1);
+        mbar_init(bar(kBarOFull), 1);
+        mbar_init(bar(kBarOEmpty), 4);
+        mbar_init(bar(kBarXchg), 128);
+        mbar_init(bar(kBarXchg + 1), 128);
+        mbar_init(bar(kBarLx), 128);
+        mbar_init(bar(kBarVTail), 1);
+        *abort_flag = 0;
+        fence_mbarrier_init_cluster();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish_pair();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&k_map);
+        prefetch_tensormap(&v_map);
+        prefetch_tensormap(&q_map);
+        prefetch_tensormap(&o_map);
+        prefetch_tensormap(&ps_map);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    // Set up without reading anything another grid writes; from here on everything may be read, and
+    // the merge kernel, which reads the plan before its own wait, may be let in.
+    pdl_wait_prerequisites();
+    pdl_launch_dependents();
+    bool plan_ok = true;
+    UnitIter iter = make_iter(p, part, plan_ok);
+    const uint32_t tmem = *tmem_slot;
+    const AbortCtl actl{abort_flag, map_to_cta(smem_u32(tmem_slot + 1), rank ^ 1u), p.wait_budget_ns};
+    const uint64_t part_pol = l2_policy_evict_last();
+    if (!plan_ok && threadIdx.x == 0) raise_error(8 /* MLA_DEVERR_BAD_METADATA */);
+
+    // A warp reporting to the leader's MMA issuer: the leader's warp arrives with expect_tx of 4
+    // bytes, the peer's warp sends a 4-byte st.async whose complete_tx lands on the leader's barrier.
+    auto signal_leader = [&](int b_idx, int word) {
+        __syncwarp();
+        if (lane == 0) {
+            if (leader)
+                mbar_arrive_expect_tx(bar(b_idx), 4);
+            else
+                st_async_b32(map_to_cta(sbase + kOffPSig + 4u * (uint32_t)word, 0), 0u,
+                             map_to_cta(bar(b_idx), 0));
+        }
+    };
+    // let copies already issued land before shared memory can go away
+    auto drain_on_abort = [&]() {
+        if (lane == 0 && *abort_flag) {
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 200000ull) {
+            }
+        }
+    };
+
+    if (warp == 0 || warp == 3) {
+        // ------------------------------------------------------------ K producers
+        const uint32_t mine = warp == 3 ? 1u : 0u;
+        uint32_t g = 0;
+        bool alive = true;
+        Unit u;
+        while (alive && iter.next(p, u)) {
+            const int n = u.tiles();
+            if (n <= 0) continue;
+            PageWindow pw;
+            pw.init(p.block_table + (int64_t)u.b * p.bt_stride, 2 * u.t0, u.kb1, lane, p.num_pages, warp == 0);
+            for (int i = 0; i < n; ++i, ++g) {
+                const int blk = 2 * (u.t0 + i) + (int)rank;
+                const int32_t row = pw.row(blk);
+                if ((g & 1u) != mine) continue;
+                int ok = 1;
+                const int s = (int)(g & 1u);
+                const uint32_t slot = sbase + kOffK + s * kKSlotBytes;
+                const bool withhold = leader && (int)g == p.withhold_tile;
+                if (lane == 0) {
+                    ok = mbar_wait_bounded(bar(kBarKEmpty + s), ((g >> 1) & 1u) ^ 1u, actl);
+                    if (ok && !withhold) {
+                        if constexpr (kFp8) {
+                            mbar_arrive_expect_tx(bar(kBarKRaw + s), kPage8Bytes);
+                            tma_load_3d(slot + kRaw8Off, &k_map, bar(kBarKRaw + s), 0, row, 0);
+                        } else {
+                            const uint32_t kf = bar(kBarKFull + s);
+                            if (leader) mbar_arrive_expect_tx(kf, 2 * kChunks * kBox);
+                            tma_load_3d_pair(slot, &k_map, map_to_cta(kf, 0), 0, row, 0);
+                        }
+                    }
+                }
+                if (!__shfl_sync(0xffffffffu, ok, 0)) {
+                    alive = false;
+                    break;
+                }
+                if constexpr (kFp8) {
+                    const bool landed = mbar_wait_bounded(bar(kBarKRaw + s), (g >> 1) & 1u, actl);
+                    if (!__all_sync(0xffffffffu, landed)) {
+                        alive = false;
+                        break;
+                    }
+                    const int valid = u.L - blk * kPage;
+#pragma unroll 1
+                    for (int c = 0; c < kChunks; ++c)
+                        widen_chunk_rows<kE5M2>(slot + kRaw8Off + c * kChunk8, slot + c * kBox, lane, valid);
+                    fence_proxy_async_smem();
+                    signal_leader(kBarKFull + s, 8);
+                }
+            }
+        }
+        drain_on_abort();
+    } else if (warp >= kQWarp0) {
+        // ------------------------------------------------------------ Q and partner V
+        const int quarter = warp & 3;
+        const int qt = threadIdx.x - kQWarp0 * 32;          // 0..127
+        const int rloc = (32 * quarter + lane) & 63;
+        const int rtile = kCtaRows * (int)rank + rloc;      // row of the unit's tile
+        const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
+        uint32_t uq = 0, g = 0, ntail = 0;
+        bool q_range = false, alive = true;
+        Unit u;
+        while (alive && iter.next(p, u)) {
+            const int n = u.tiles();
+            if (n <= 0) continue;
+            // ---- Q of the unit (rows past its last read as zeros)
+            if (uq > 0 && !mbar_wait_bounded(bar(kBarQEmpty), (uq - 1) & 1u, actl)) break;
+            tc_fence_after();
+            if (!kFp8 && quarter == 3 && lane == 0) {
+                if (leader) mbar_arrive_expect_tx(bar(kBarQFull), 2 * kQHiBytes);
+                tma_load_3d_pair(sbase + kOffQ, &q_map, map_to_cta(bar(kBarQFull), 0), 0,
+                                 u.row0 + kCtaRows * (int)rank, kQLoChunks);
+            }
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)u.row0 + rtile) * kDqk);
+            const bool have = rtile < u.nrows;
+            {
+                uint4 v[32];   // the row's columns [0, 256): all loads in flight at once
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = have ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        w[4 * k] = v[4 * c + k].x;
+                        w[4 * k + 1] = v[4 * c + k].y;
+                        w[4 * k + 2] = v[4 * c + k].z;
+                        w[4 * k + 3] = v[4 * c + k].w;
+                    }
+                    if constexpr (kFp8) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) w[k] = decode::bf16x2_to_f16x2(w[k], q_range);
+                    }
+                    tmem_st16(tmem + lane_off + kTmemQ + 16u * c, w);
+                }
+            }
+            if constexpr (kFp8) {
+                // Q columns [256, 576) as f16 into shared memory (128-byte swizzle): lane
+                // quarters 0 / 1 take chunks 0..2 of them, quarters 2 / 3 chunks 3..4
+                const int c0 = quarter < 2 ? 0 : 3, c1 = quarter < 2 ? 3 : kQHiChunks;
+#pragma unroll 1
+                for (int cc = c0; cc < c1; ++cc) {
+                    const uint32_t qrow = sbase + kOffQ + cc * kBox + (uint32_t)rloc * 128u;
+                    uint4 v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = have ? __ldg(src + 32 + 8 * cc + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        st_shared_v4u(qrow + 16u * ((uint32_t)k ^ ((uint32_t)rloc & 7u)),
+                                      decode::bf16x2_to_f16x2(v[k].x, q_range), decode::bf16x2_to_f16x2(v[k].y, q_range),
+                                      decode::bf16x2_to_f16x2(v[k].z, q_range), decode::bf16x2_to_f16x2(v[k].w, q_range));
+                }
+                fence_proxy_async_smem();
+                if (__any_sync(0xffffffffu, q_range) && lane == 0) raise_error(32 /* MLA_DEVERR_Q_RANGE */);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            signal_leader(kBarQFull, 9 + quarter);
+            ++uq;
+            // ---- partner V of each tile of the unit
+            const int32_t* bt_row = p.block_table + (int64_t)u.b * p.bt_stride;
+            for (int i = 0; i < n; ++i, ++g) {
+                const int blk = 2 * (u.t0 + i) + 1 - (int)rank;
+                int pg = blk < u.kb1 ? __ldg(bt_row + blk) : -1;
+                if (pg < 0 || (int64_t)pg >= p.num_pages) pg = -1;   // reported by the K loads
+                const int s = (int)(g & 1u);
+                const uint32_t slot = sbase + kOffK + s * kKSlotBytes;
+                if constexpr (!kFp8) {
+                    if (quarter == 3) {
+                        // two 16 KB loads once the tile's S MMAs are done.  A tile whose pages reach
+                        // past L: the rows there are cleared, in this CTA's own V chunks and in the
+                        // partner's once they landed, before the leader is told.
+                        const int own_valid = u.L - (blk ^ 1) * kPage, valid = u.L - blk * kPage;
+                        const bool cut = (own_valid < kPage && (blk ^ 1) < u.kb1) || (valid < kPage && blk < u.kb1);
+                        int ok = 1;
+                        if (lane == 0) {
+                            ok = mbar_wait_bounded(bar(kBarQKDone + s), (g >> 1) & 1u, actl);
+                            if (ok) {
+                                const int32_t row = pg >= 0 ? pg * kPage : (int32_t)(p.num_pages * kPage);
+                                if (cut)
+                                    mbar_arrive_expect_tx(bar(kBarVTail), 2 * 2 * kBox);
+                                else if (leader)
+                                    mbar_arrive_expect_tx(bar(kBarVFull + s), 2 * 2 * 2 * kBox);
+#pragma unroll
+                                for (int nn = 0; nn < 2; ++nn) {
+                                    const uint32_t dst = slot + (4 * nn + 2 * (1 - (int)rank)) * kBox;
+                                    if (cut)
+                                        tma_load_3d(dst, &v_map, bar(kBarVTail), 0, row, 4 * nn + 2 * (int)rank);
+                                    else
+                                        tma_load_3d_pair(dst, &v_map, map_to_cta(bar(kBarVFull + s), 0), 0, row,
+                                                         4 * nn + 2 * (int)rank);
+                                }
+                            }
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (ok && cut) {
+                            if (own_valid < kPage) clear_v_rows(slot, 2 * (int)rank, own_valid, lane);
+                            const bool landed = mbar_wait_bounded(bar(kBarVTail), ntail & 1u, actl);
+                            ok = __all_sync(0xffffffffu, landed);
+                            if (valid < kPage) clear_v_rows(slot, 2 * (1 - (int)rank), valid, lane);
+                            fence_proxy_async_smem();
+                            signal_leader(kBarVFull + s, 4);
+                            ++ntail;
+                        }
+                        if (!ok) {
+                            alive = false;
+                            break;
+                        }
+                    }
+                } else {
+                    // 4 chunks x 64 rows x 4 sixteen-byte units of 8-bit values: 8 per thread,
+                    // widened to f16 on the way into the slot, rows at or past L as zeros
+                    const int valid = u.L - blk * kPage;
+                    uint4 v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int x = qt + 128 * j, hh = x >> 8, row = (x >> 2) & 63, q4 = x & 3;
+                        const int chunk = 4 * (hh >> 1) + 2 * (int)rank + (hh & 1);
+                        v[j] = pg >= 0 && row < valid ? __ldg(reinterpret_cast<const uint4*>(
+                                             p.kv + ((int64_t)pg * kPage + row) * kDqk + chunk * 64 + q4 * 16))
+                                       : make_uint4(0, 0, 0, 0);
+                    }
+                    const bool done = mbar_wait_bounded(bar(kBarQKDone + s), (g >> 1) & 1u, actl);
+                    if (!__all_sync(0xffffffffu, done)) {
+                        alive = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int x = qt + 128 * j, hh = x >> 8, row = (x >> 2) & 63, q4 = x & 3;
+                        const int pos = 4 * (hh >> 1) + 2 * (1 - (int)rank) + (hh & 1);
+                        const uint32_t r = slot + pos * kBox + row * 128;
+                        const uint32_t sw = (uint32_t)row & 7u;
+                        st_shared_v4u(r + 16u * ((2u * q4) ^ sw), fp8x2_to_f16x2<kE5M2>(v[j].x),
+                                      fp8x2_to_f16x2<kE5M2>(v[j].x >> 16), fp8x2_to_f16x2<kE5M2>(v[j].y),
+                                      fp8x2_to_f16x2<kE5M2>(v[j].y >> 16));
+                        st_shared_v4u(r + 16u * ((2u * q4 + 1u) ^ sw), fp8x2_to_f16x2<kE5M2>(v[j].z),
+                                      fp8x2_to_f16x2<kE5M2>(v[j].z >> 16), fp8x2_to_f16x2<kE5M2>(v[j].w),
+                                      fp8x2_to_f16x2<kE5M2>(v[j].w >> 16));
+                    }
+                    fence_proxy_async_smem();
+                    signal_leader(kBarVFull + s, 4 + quarter);
+                }
+            }
+        }
+        if (!kFp8 && quarter == 3) drain_on_abort();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (leader)
+        // Two cursors walk the same tiles: S(t) = Q K^T and O += P(t) V(t); whichever is ready goes
+        // first, PV before S.  The whole warp walks, an elected lane issues each MMA.
+        if (leader) {
+            auto poll = [](uint32_t b, uint32_t parity) -> bool {
+                return __all_sync(0xffffffffu, mbar_test_wait(b, parity));
+            };
+            struct Cursor {
+                UnitIter it;
+                int n, i;
+                uint32_t g, uq;
+                bool valid;
+                __device__ void next_unit(const Params& pp) {
+                    Unit v;
+                    valid = false;
+                    while (it.next(pp, v)) {
+                        n = v.tiles();
+                        if (n > 0) {
+                            i = 0;
+                            valid = true;
+                            return;
+                        }
+                    }
+                }
+                __device__ void step(const Params& pp) {
+                    ++g;
+                    if (++i == n) {
+                        ++uq;
+                        next_unit(pp);
+                    }
+                }
+            };
+            Cursor cq, cp;
+            cq.it = iter;
+            cq.g = 0;
+            cq.uq = 0;
+            cq.n = cq.i = 0;
+            cq.next_unit(p);
+            cp = cq;
+            uint64_t t_idle = global_timer_ns();
+            while (cq.valid || cp.valid) {
+                bool did = false;
+                if (cp.valid && cp.g < cq.g) {
+                    const int s = (int)(cp.g & 1u);
+                    const bool first = cp.i == 0;
+                    if (poll(bar(kBarPFull), cp.g & 1u) && poll(bar(kBarVFull + s), (cp.g >> 1) & 1u) &&
+                        (!first || cp.uq == 0 || poll(bar(kBarOEmpty), (cp.uq - 1) & 1u))) {
+                        tc_fence_after();
+                        const uint32_t pbuf = sbase + kOffP;
+                        const uint32_t slot = sbase + kOffK + s * kKSlotBytes;
+#pragma unroll
+                        for (int nn = 0; nn < 2; ++nn)
+#pragma unroll
+                            for (int pp = 0; pp < 2; ++pp)
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    mma_pair_ss(tmem + kTmemO + 128u * nn,
+                                                smem_desc_sw128(pbuf + pp * kBox + 32u * kk, 16, 1024),
+                                                smem_desc_sw128(slot + (4 * nn + 2 * pp) * kBox + 2048u * kk, kBox, 1024),
+                                                kFp8 ? kIdescPV16 : kIdescPV, (first && pp == 0 && kk == 0) ? 0u : 1u);
+                        tc_commit_pair(bar(kBarKEmpty + s));
+                        tc_commit_pair(bar(kBarPvDone));
+                        if (cp.i == cp.n - 1) tc_commit_pair(bar(kBarOFull));
+                        cp.step(p);
+                        did = true;
+                    }
+                }
+                if (!did && cq.valid) {
+                    const int s = (int)(cq.g & 1u);
+                    const uint32_t sb = cq.g & 1u;
+                    if ((cq.i != 0 || poll(bar(kBarQFull), cq.uq & 1u)) &&
+                        (cq.g < 2 || poll(bar(kBarSFree + sb), ((cq.g >> 1) & 1u) ^ 1u)) &&
+                        poll(bar(kBarKFull + s), (cq.g >> 1) & 1u)) {
+                        tc_fence_after();
+                        const uint32_t slot = sbase + kOffK + s * kKSlotBytes;
+                        const uint32_t d = tmem + kTmemS + 64u * sb;
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c) {
+                            if (c < kQLoChunks) {
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    mma_pair_ts(d, tmem + kTmemQ + 32u * c + 8u * kk,
+                                                smem_desc_sw128(slot + c * kBox + 32u * kk, 16, 1024),
+                                                kFp8 ? kIdescQK16 : kIdescQK, (c | kk) ? 1u : 0u);
+                            } else {
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    mma_pair_ss(d, smem_desc_sw128(sbase + kOffQ + (c - kQLoChunks) * kBox + 32u * kk, 16, 1024),
+                                                smem_desc_sw128(slot + c * kBox + 32u * kk, 16, 1024),
+                                                kFp8 ? kIdescQK16 : kIdescQK, 1u);
+                            }
+                        }
+                        tc_commit_pair(bar(kBarQKDone + s));
+                        tc_commit_pair(bar(kBarSFull + sb));
+                        if (cq.i == cq.n - 1) tc_commit_pair(bar(kBarQEmpty));
+                        cq.step(p);
+                        did = true;
+                    }
+                }
+                if (did) {
+                    t_idle = global_timer_ns();
+                } else {
+                    if (*abort_flag) break;
+                    if (global_timer_ns() - t_idle > actl.budget_ns) {
+                        if (lane == 0) raise_abort(actl);
+                        break;
+                    }
+                }
+            }
+        }
+    } else if (warp >= kSoftmaxWarp0 && warp < kSoftmaxWarp0 + 4) {
+        // ------------------------------------------------------------ softmax / epilogue
+        const int t = threadIdx.x - kSoftmaxWarp0 * 32;       // TMEM lane
+        const int rloc = t & 63;                              // row within this CTA's 64
+        const int half = t >> 6;                              // token half of each tile
+        const uint32_t lane_off = (uint32_t)((warp - kSoftmaxWarp0) * 32) << 16;
+        const int rtile = kCtaRows * (int)rank + rloc;        // row of the unit's tile
+        const float dq = p.descale_q ? *p.descale_q : 1.0f;
+        const float dk = p.descale_k ? *p.descale_k : 1.0f;
+        const float sl2 = p.scale_log2 * dq * dk;
+        float* xmax = reinterpret_cast<float*>(smem + kOffX);  // [2][128] row maxima, [128] sums
+        const uint32_t swz = (uint32_t)(rloc & 7);
+
+        uint32_t g = 0, uq = 0;
+        bool alive = true;
+        Unit u;
+        while (alive && iter.next(p, u)) {
+            const int n = u.tiles();
+            const bool row_valid = rtile < u.nrows;
+            if (n <= 0) {
+                // no key at all: o = 0, lse = -inf
+                if (row_valid) {
+                    __nv_bfloat16* row_out = p.out + ((int64_t)u.row0 + rtile) * kDv + 256 * half;
+                    for (int c = 0; c < 32; ++c) reinterpret_cast<uint4*>(row_out)[c] = make_uint4(0, 0, 0, 0);
+                    if (half == 0) p.lse[(int64_t)u.row0 + rtile] = -INFINITY;
+                }
+                continue;
+            }
+            int lim = u.L;
+            if (p.causal) {
+                const int64_t l = (int64_t)u.L - u.n + (u.row_in_req + rtile) / p.h + 1;
+                lim = l < u.L ? (int)l : u.L;
+            }
+            if (lim > u.kb1 * kPage) lim = u.kb1 * kPage;   // keys of this piece (and of the table) only
+            float m_run = -INFINITY, l_half = 0.f;
+            for (int i = 0; i < n; ++i, ++g) {
+                const uint32_t sb = g & 1u;
+                if (!mbar_wait_bounded(bar(kBarSFull + sb), (g >> 1) & 1u, actl)) {
+                    alive = false;
+                    break;
+                }
+                tc_fence_after();
+                float s[64];
+                {
+                    uint32_t raw[4][16];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tmem_ld16(tmem + lane_off + kTmemS + 64u * sb + 16u * c, raw[c]);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) s[16 * c + k] = __uint_as_float(raw[c][k]);
+                }
+                tc_fence_before();
+                signal_leader(kBarSFree + sb, 16 + (warp - kSoftmaxWarp0));
+                // scale to log2 units, mask the keys at or past the limit, this half's maximum
+                const int kbase = (u.t0 + i) * kTileKeys + kPage * half;
+#pragma unroll
+                for (int j = 0; j < 64; j += 2) mul2(s[j], s[j + 1], sl2);
+                if (kbase + 64 > lim) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        if (kbase + j >= lim) s[j] = -INFINITY;
+                }
+                float hmax;
+                {
+                    float m0 = fmaxf(s[0], s[1]), m1 = fmaxf(s[2], s[3]);
+#pragma unroll
+                    for (int j = 4; j < 64; j += 4) {
+                        m0 = fmax3(m0, s[j], s[j + 1]);
+                        m1 = fmax3(m1, s[j + 2], s[j + 3]);
+                    }
+                    hmax = fmaxf(m0, m1);
+                }
+                // partner thread t ^ 64 holds the other 64 tokens of this row
+                xmax[sb * 128 + t] = hmax;
+                mbar_arrive(bar(kBarXchg + sb));
+                if (!mbar_wait_bounded(bar(kBarXchg + sb), (g >> 1) & 1u, actl)) {
+                    alive = false;
+                    break;
+                }
+                const float tmax = fmaxf(hmax, xmax[sb * 128 + (t ^ 64)]);
+                const float m_new = fmaxf(m_run, tmax);
+                const bool rescale = m_new > m_run + kRescaleThreshold;
+                float factor = 1.f;
+                if (rescale) {
+                    factor = fast_exp2(m_run - m_new);  // 0 when m_run = -inf
+                    l_half *= factor;
+                    m_run = m_new;
+                }
+                // P packed in pairs into s[0..31]; zeros while every key so far is masked
+                if (m_run != -INFINITY) {
+                    float ps0 = 0.f, ps1 = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        float p0 = s[2 * j], p1 = s[2 * j + 1];
+                        sub2(p0, p1, m_run);
+                        p0 = fast_exp2(p0);
+                        p1 = fast_exp2(p1);
+                        add2(ps0, ps1, p0, p1);
+                        s[j] = __uint_as_float(kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1));
+                    }
+                    l_half += ps0 + ps1;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) s[j] = 0.f;
+                }
+                // the P buffer is free, and O holds every PV up to tile g - 1, once PV(g - 1) is done
+                if (g >= 1 && !mbar_wait_bounded(bar(kBarPvDone), (g - 1) & 1u, actl)) {
+                    alive = false;
+                    break;
+                }
+                if (i > 0 && __any_sync(0xffffffffu, rescale)) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 16; ++c) {
+                        uint32_t raw[16];
+                        tmem_ld16(tmem + lane_off + kTmemO + 16u * c, raw);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            raw[k] = __float_as_uint(__uint_as_float(raw[k]) * factor);
+                        tmem_st16(tmem + lane_off + kTmemO + 16u * c, raw);
+                    }
+                    tc_wait_st();
+                    tc_fence_before();
+                }
+                // P -> shared memory, K-major with 128-byte swizzle
+                {
+                    const uint32_t prow = sbase + kOffP + half * kBox + rloc * 128u;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        st_shared_v4u(prow + ((c ^ swz) << 4), __float_as_uint(s[4 * c]),
+                                      __float_as_uint(s[4 * c + 1]), __float_as_uint(s[4 * c + 2]),
+                                      __float_as_uint(s[4 * c + 3]));
+                }
+                fence_proxy_async_smem();
+                signal_leader(kBarPFull, warp - kSoftmaxWarp0);
+            }
+            if (!alive) break;
+            // ---- epilogue of the unit: o (or the piece's fp32 partial, normalised) and lse
+            if (!mbar_wait_bounded(bar(kBarOFull), uq & 1u, actl)) break;
+            tc_fence_after();
+            xmax[256 + t] = l_half;
+            mbar_arrive(bar(kBarLx));
+            if (!mbar_wait_bounded(bar(kBarLx), uq & 1u, actl)) break;
+            const float l_run = l_half + xmax[256 + (t ^ 64)];
+            const float inv = l_run > 0.f ? dk / l_run : 0.f;
+            const float lse_val = l_run > 0.f ? (m_run + __log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+            const bool direct = u.slot < 0;
+            {
+                // 64 tensor-memory columns a step, staged 32 rows x 128 bytes at a time (128-byte
+                // swizzle): the warp's own 4 KB and its 4 KB of the P buffer, idle now, alternate.
+                const uint32_t stage_a = sbase + kOffStage + (uint32_t)(warp - kSoftmaxWarp0) * 4096u;
+                const uint32_t stage_b = sbase + kOffP + (uint32_t)(warp - kSoftmaxWarp0) * 4096u;
+                uint32_t npass = 0;
+                const int r0 = kCtaRows * (int)rank + 32 * ((warp - kSoftmaxWarp0) & 1);   // the warp's first row
+                const int rows = min(32, u.nrows - r0);   // of its rows in the unit (<= 0: none)
+#pragma unroll 1
+                for (int st = 0; st < 4; ++st) {
+                    uint32_t raw[64];
+                    tmem_ld16(tmem + lane_off + kTmemO + 64u * st, *reinterpret_cast<uint32_t(*)[16]>(raw));
+                    tmem_ld16(tmem + lane_off + kTmemO + 64u * st + 16u, *reinterpret_cast<uint32_t(*)[16]>(raw + 16));
+                    tmem_ld16(tmem + lane_off + kTmemO + 64u * st + 32u, *reinterpret_cast<uint32_t(*)[16]>(raw + 32));
+                    tmem_ld16(tmem + lane_off + kTmemO + 64u * st + 48u, *reinterpret_cast<uint32_t(*)[16]>(raw + 48));
+                    tc_wait_ld();
+                    if (st == 3) {
+                        tc_fence_before();
+                        signal_leader(kBarOEmpty, 20 + (warp - kSoftmaxWarp0));   // O is free for the next unit
+                    }
+#pragma unroll
+                    for (int pass = 0; pass < 2; ++pass) {
+                        if (direct && pass == 1) break;
+                        uint32_t w[32];
+                        int col = 256 * (st >> 1) + 128 * half + 64 * (st & 1);
+                        if (direct) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                w[k] = pack_bf16x2(__uint_as_float(raw[2 * k]) * inv, __uint_as_float(raw[2 * k + 1]) * inv);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(__uint_as_float(raw[32 * pass + k]) * inv);
+                            col += 32 * pass;
+                        }
+                        const uint32_t stage = (npass & 1u) ? stage_b : stage_a;
+                        if (lane == 0 && npass >= 2) bulk_wait_read<1>();
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            st_shared_v4u(stage + (uint32_t)lane * 128u + 16u * ((uint32_t)k ^ ((uint32_t)lane & 7u)),
+                                          w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (!direct || rows == 32) {
+                            // whole boxes go out as TMA stores (a partial's slot always has room for one)
+                            if (lane == 0) {
+                                if (direct)
+                                    tma_store_2d(&o_map, stage, col, u.row0 + r0);
+                                else
+                                    tma_store_2d_hint(&ps_map, stage, col, u.slot * kTileRows + r0, part_pol);
+                                bulk_commit();
+                            }
+                        } else {
+                            // the rows behind belong to another request or to nobody
+                            for (int r = lane >> 3; r < rows; r += 4) {
+                                const uint4 v = ld_shared_v4u(stage + (uint32_t)r * 128u + 16u * (((uint32_t)lane & 7u) ^ ((uint32_t)r & 7u)));
+                                *reinterpret_cast<uint4*>(p.out + ((int64_t)u.row0 + r0 + r) * kDv + col + 8 * (lane & 7)) = v;
+                            }
+                        }
+                        ++npass;
+                        __syncwarp();
+                    }
+                }
+            }
+            if (lane == 0) bulk_wait_read<0>();   // the staging (and the P buffer) free again
+            __syncwarp();
+            if (half == 0) {
+                if (!direct)
+                    st_global_f32_hint(p.part_lse + (int64_t)u.slot * kTileRows + rtile, row_valid ? lse_val : -INFINITY, part_pol);
+                else if (row_valid)
+                    p.lse[(int64_t)u.row0 + rtile] = lse_val;
+            }
+            ++uq;
+        }
+        if (lane == 0) bulk_wait<0>();   // the epilogues' stores
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+// Join the pieces of the units that the plan cut: lse = ln sum_i exp(lse_i), o = sum_i
+// exp(lse_i - lse) o_i, in part order.  Part i begins a cut unit when its end lies inside a unit
+// that it does not itself continue; its piece is slot 2 i + 1, and the parts after it that begin
+// inside the same unit hold the others in slot 2 j.  Every CTA lists the cut units from the plan
+// (before it waits for the attention grid: the plan is older than that grid), then the warps take
+// (unit, row, 128-column slice) in turn.  At most 2 x 256 KB of partials a part: latency bounds it.
+constexpr int kMergeThreads = 256;
+constexpr int kMergeMaxParts = 1024;
+constexpr int kMergeSlices = 4;   // 128 columns a warp, four a lane
+
+__global__ void __launch_bounds__(kMergeThreads)
+chunk_merge_kernel(const int32_t* __restrict__ plan, const int32_t* __restrict__ cu, int32_t parts, int32_t bs, int32_t h,
+                   int32_t num_tokens, const float* __restrict__ part_o, const float* __restrict__ part_lse,
+                   __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+    __shared__ int2 task[kMergeMaxParts];   // part that begins the unit, parts that continue it
+    __shared__ int ntask;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x < 32) {   // in part order: every CTA must number the units alike
+        int count = 0;
+        for (int i0 = 0; i0 < parts; i0 += 32) {
+            const int i = i0 + lane;
+            int n = 0;
+            if (i < parts) {
+                const int32_t* r = plan + 8 * (int64_t)i;
+                const int b = r[3], m = r[4], t = r[5];
+                const bool continues = r[0] == b && r[1] == m && (r[2] > 0 || r[2] >= t);
+                if (t > 0 && b >= 0 && b < bs && m >= 0 && !continues) {
+                    for (const int32_t* e = r + 8; i + 1 + n < parts && e[0] == b && e[1] == m && e[2] > 0; e += 8) ++n;
+                }
+            }
+            const unsigned found = __ballot_sync(0xffffffffu, n > 0);
+            if (n > 0) task[count + __popc(found & ((1u << lane) - 1u))] = make_int2(i, n);
+            count += __popc(found);
+        }
+        if (lane == 0) ntask = count;
+    }
+    __syncthreads();
+    pdl_wait_prerequisites();
+    const int64_t total = (int64_t)ntask * kTileRows * kMergeSlices;
+    const int64_t nwarps = (int64_t)gridDim.x * (kMergeThreads / 32);
+    for (int64_t w = (int64_t)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5); w < total; w += nwarps) {
+        const int slice = (int)(w % kMergeSlices);
+        const int row = (int)(w / kMergeSlices % kTileRows);
+        const int2 tk = task[w / (kMergeSlices * kTileRows)];
+        const int32_t* r = plan + 8 * (int64_t)tk.x;
+        int c0, n;
+        request_rows(cu, r[3], num_tokens, c0, n);
+        if ((int64_t)r[4] * kTileRows + row >= (int64_t)n * h) continue;
+        const int64_t orow = (int64_t)c0 * h + (int64_t)r[4] * kTileRows + row;
+        const int pieces = tk.y + 1;
+        auto slot_of = [&](int k) { return (int64_t)(k == 0 ? 2 * tk.x + 1 : 2 * (tk.x + k)); };
+        auto lse_of = [&](int k) -> float {
+            if (k > 0) {   // a part that begins inside the unit but holds none of it
+                const int32_t* e = plan + 8 * (int64_t)(tk.x + k);
+                if (e[0] == e[3] && e[1] == e[4] && e[2] >= e[5]) return -INFINITY;
+            }
+            return part_lse[slot_of(k) * kTileRows + row];
+        };
+        float mx = -INFINITY;
+        for (int k = lane; k < pieces; k += 32) mx = fmaxf(mx, lse_of(k));
+        for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        float sum = 0.f;
+        if (mx != -INFINITY)
+            for (int k = lane; k < pieces; k += 32) sum += expf(lse_of(k) - mx);
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const float total_lse = mx != -INFINITY ? mx + logf(sum) : -INFINITY;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int col = slice * 128 + 4 * lane;
+        if (mx != -INFINITY) {
+            for (int k0 = 0; k0 < pieces; k0 += 8) {
+                float4 v[8];
+                float wt[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int k = k0 + j;
+                    const float l = k < pieces ? lse_of(k) : -INFINITY;
+                    wt[j] = l != -INFINITY ? expf(l - total_lse) : 0.f;
+                    v[j] = l != -INFINITY ? *reinterpret_cast<const float4*>(part_o + (slot_of(k) * kTileRows + row) * kDv + col)
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    acc.x += wt[j] * v[j].x;
+                    acc.y += wt[j] * v[j].y;
+                    acc.z += wt[j] * v[j].z;
+                    acc.w += wt[j] * v[j].w;
+                }
+            }
+        }
+        *reinterpret_cast<uint2*>(out + orow * kDv + col) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+        if (slice == 0 && lane == 0) lse[orow] = total_lse;
+    }
+}
+
+}  // namespace chunk
+}  // namespace mla

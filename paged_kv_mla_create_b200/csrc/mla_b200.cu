@@ -15,6 +15,7 @@
 
 #include "../../include/mla_b200.h"
 #include "block_table.cuh"
+#include "chunk.cuh"
 #include "combine.cuh"
 #include "decode.cuh"
 #include "extend.cuh"
@@ -76,6 +77,27 @@ mla_status_t prepare_decode_kernels() {
             if (results[dev] == cudaSuccess)
                 results[dev] = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                     mla::decode::kSmemBytes);
+    });
+    return from_cuda(results[dev]);
+}
+
+// The same for the ragged attention kernels.
+mla_status_t prepare_chunk_kernels() {
+    static std::once_flag flags[kMaxDevices];
+    static cudaError_t results[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return MLA_ERR_CUDA;
+    if (dev < 0 || dev >= kMaxDevices) return MLA_ERR_UNSUPPORTED;
+    std::call_once(flags[dev], [dev] {
+        const void* kernels[] = {reinterpret_cast<const void*>(mla::chunk::mla_chunk_kernel<0>),
+                                 reinterpret_cast<const void*>(mla::chunk::mla_chunk_kernel<1>),
+                                 reinterpret_cast<const void*>(mla::chunk::mla_chunk_kernel<2>)};
+        results[dev] = cudaSuccess;
+        for (const void* k : kernels)
+            if (results[dev] == cudaSuccess)
+                results[dev] = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    mla::chunk::kSmemBytes);
     });
     return from_cuda(results[dev]);
 }
@@ -589,6 +611,196 @@ mla_status_t mla_extend_paged_prefix(const void* q, int32_t bs, int32_t e, int32
     // (3) merge_state
     return mla_merge_state(at(L.o1), reinterpret_cast<const float*>(at(L.lse1)), at(L.o2),
                            reinterpret_cast<const float*>(at(L.lse2)), (int64_t)rows, 512, out, lse, stream);
+}
+
+mla_status_t mla_build_chunk_metadata(
+    int32_t* req_to_token, int64_t req_to_token_rows, int64_t req_to_token_stride, const void* req_pool_indices,
+    int32_t index_dtype, const void* prefix_lens, const void* chunk_lens, int32_t lens_dtype, int32_t bs,
+    int32_t num_tokens, const void* free_pages, int64_t num_free_pages, int32_t num_heads, int32_t causal,
+    int32_t num_parts, int32_t* block_table, int64_t block_table_stride, int32_t max_pages, int32_t page_size,
+    int32_t fill_tail, int32_t pad_slot, int32_t* cache_seqlens, int32_t* cu_seqlens, int32_t* positions,
+    int32_t* cache_loc, int32_t* chunk_plan, int32_t* pages_taken, mla_stream_t stream) {
+    const NvtxRange nvtx_range("mla_build_chunk_metadata");
+    using namespace mla::chunk;
+    if (bs < 0 || num_tokens < 0 || max_pages < 0 || page_size != 64 || num_heads <= 0) return MLA_ERR_INVALID_ARG;
+    if (num_parts < 1 || num_parts > kMergeMaxParts || (causal != 0 && causal != 1)) return MLA_ERR_INVALID_ARG;
+    if (index_dtype != MLA_DTYPE_INT32 && index_dtype != MLA_DTYPE_INT64) return MLA_ERR_INVALID_ARG;
+    if (lens_dtype != MLA_DTYPE_INT32 && lens_dtype != MLA_DTYPE_INT64) return MLA_ERR_INVALID_ARG;
+    if (num_free_pages < 0 || (free_pages && num_free_pages > INT32_MAX)) return MLA_ERR_INVALID_ARG;
+    if (!cu_seqlens || !chunk_plan) return MLA_ERR_INVALID_ARG;
+    if (!is_aligned(chunk_plan, 16)) return MLA_ERR_INVALID_ARG;
+    if (bs > 0 && (!req_to_token || !req_pool_indices || !prefix_lens || !chunk_lens || !cache_seqlens ||
+                   (max_pages > 0 && !block_table)))
+        return MLA_ERR_INVALID_ARG;
+    if (num_tokens > 0 && (!positions || !cache_loc)) return MLA_ERR_INVALID_ARG;
+    if (bs > 0 && (req_to_token_rows <= 0 || req_to_token_stride <= 0 || block_table_stride < max_pages))
+        return MLA_ERR_INVALID_ARG;
+    if (bs > kMetaMaxRequests || (int64_t)num_tokens * num_heads > INT32_MAX - 256) return MLA_ERR_UNSUPPORTED;
+    MetaParams a;
+    a.req_to_token = req_to_token;
+    a.r2t_rows = req_to_token_rows;
+    a.r2t_stride = req_to_token_stride;
+    a.rpi = req_pool_indices;
+    a.prefix_lens = prefix_lens;
+    a.chunk_lens = chunk_lens;
+    a.bs = bs;
+    a.num_tokens = num_tokens;
+    a.max_pages = max_pages;
+    a.num_heads = num_heads;
+    a.free_pages = free_pages;
+    a.num_free = free_pages ? num_free_pages : 0;
+    a.causal = causal;
+    a.pad_slot = pad_slot;
+    a.fill_tail = fill_tail;
+    a.parts = num_parts;
+    a.block_table = block_table;
+    a.bt_stride = block_table_stride;
+    a.cache_seqlens = cache_seqlens;
+    a.cu_seqlens = cu_seqlens;
+    a.positions = positions;
+    a.cache_loc = cache_loc;
+    a.plan = chunk_plan;
+    a.pages_taken = pages_taken;
+    const int64_t table_ctas = ((int64_t)bs * max_pages + kMetaPerCta - 1) / kMetaPerCta;
+    const int64_t token_ctas = ((int64_t)num_tokens + kMetaPerCta - 1) / kMetaPerCta;
+    if (1 + table_ctas + token_ctas > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+    a.table_ctas = (int32_t)table_ctas;
+    const unsigned grid = (unsigned)(1 + table_ctas + token_ctas);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const bool i64 = index_dtype == MLA_DTYPE_INT64, l64 = lens_dtype == MLA_DTYPE_INT64;
+    if (i64 && l64) chunk_metadata_kernel<int64_t, int64_t><<<grid, kMetaThreads, 0, st>>>(a);
+    else if (i64) chunk_metadata_kernel<int64_t, int32_t><<<grid, kMetaThreads, 0, st>>>(a);
+    else if (l64) chunk_metadata_kernel<int32_t, int64_t><<<grid, kMetaThreads, 0, st>>>(a);
+    else chunk_metadata_kernel<int32_t, int32_t><<<grid, kMetaThreads, 0, st>>>(a);
+    return from_cuda(cudaGetLastError());
+}
+
+int32_t mla_num_chunk_parts(int32_t sm_count) {
+    if (sm_count <= 0) return -1;
+    const int32_t parts = sm_count / 2;
+    return parts < 1 ? 1 : (parts > mla::chunk::kMergeMaxParts ? mla::chunk::kMergeMaxParts : parts);
+}
+
+size_t mla_chunk_workspace_bytes(int32_t num_parts) {
+    if (num_parts <= 0 || num_parts > mla::chunk::kMergeMaxParts) return 0;
+    return align256(mla::chunk::part_o_floats(num_parts) * sizeof(float)) +
+           align256((size_t)num_parts * 2 * mla::chunk::kTileRows * sizeof(float));
+}
+
+mla_status_t mla_chunk_paged(const void* q, int32_t q_dtype, int32_t num_tokens, int32_t h_q, int32_t head_dim,
+                             int32_t head_dim_v, const void* k_cache, int32_t kv_dtype, int64_t num_pages,
+                             int32_t page_size, const int32_t* block_table, int64_t block_table_stride,
+                             int32_t max_pages, const int32_t* cache_seqlens, const int32_t* cu_seqlens, int32_t bs,
+                             const int32_t* chunk_plan, int32_t num_parts, float softmax_scale, int32_t causal,
+                             const float* descale_q, const float* descale_k, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, mla_stream_t stream) {
+    const NvtxRange nvtx_range("mla_chunk_paged");
+    using namespace mla::chunk;
+    if (bs < 0 || num_tokens < 0 || h_q <= 0) return MLA_ERR_INVALID_ARG;
+    if (num_parts < 1 || num_parts > kMergeMaxParts) return MLA_ERR_INVALID_ARG;
+    if (head_dim != 576 || head_dim_v != 512 || page_size != 64) return MLA_ERR_UNSUPPORTED;
+    if (q_dtype != MLA_DTYPE_BF16) return q_dtype == MLA_DTYPE_FP8_E4M3 ? MLA_ERR_UNSUPPORTED : MLA_ERR_INVALID_ARG;
+    if (kv_dtype != MLA_DTYPE_BF16 && kv_dtype != MLA_DTYPE_FP8_E4M3 && kv_dtype != MLA_DTYPE_FP8_E5M2)
+        return MLA_ERR_INVALID_ARG;
+    if (kv_dtype == MLA_DTYPE_BF16 && descale_k) return MLA_ERR_INVALID_ARG;  // 8-bit caches only
+    if (causal != 0 && causal != 1) return MLA_ERR_INVALID_ARG;
+    if (!std::isfinite(softmax_scale)) return MLA_ERR_INVALID_ARG;
+    if (bs == 0 || num_tokens == 0) return MLA_OK;
+    if (!q || !k_cache || !block_table || !cache_seqlens || !cu_seqlens || !chunk_plan || !out || !lse)
+        return MLA_ERR_INVALID_ARG;
+    if (num_pages <= 0 || num_pages * 64 >= (int64_t(1) << 31)) return MLA_ERR_INVALID_ARG;
+    if (max_pages <= 0 || block_table_stride < max_pages) return MLA_ERR_INVALID_ARG;
+    if ((int64_t)num_tokens * h_q > INT32_MAX - 256) return MLA_ERR_UNSUPPORTED;
+    if (!is_aligned(q, 16) || !is_aligned(k_cache, 16) || !is_aligned(out, 16) || !is_aligned(chunk_plan, 16))
+        return MLA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < mla_chunk_workspace_bytes(num_parts) || !is_aligned(workspace, 256))
+        return MLA_ERR_WORKSPACE;
+    mla_status_t st = prepare_chunk_kernels();
+    if (st != MLA_OK) return st;
+    EncodeTiledFn encode = encode_tiled();
+    if (!encode) return MLA_ERR_CUDA;
+
+    // Tensor maps, as mla_decode_paged's: K pages as nine 64-column chunks, V as two-chunk boxes, q
+    // rows (64 columns, rows, 9 chunks) in boxes of 64 rows x columns [256, 576), o rows and partial
+    // rows as 32-row x 128-byte boxes (128-byte swizzle).
+    const int32_t rows = num_tokens * h_q;
+    CUtensorMap k_map, v_map, q_map, o_map, ps_map;
+    const cuuint64_t pool_rows = (cuuint64_t)num_pages * 64;
+    const cuuint32_t es[3] = {1, 1, 1};
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    float* part_o = reinterpret_cast<float*>(ws);
+    float* part_lse = reinterpret_cast<float*>(ws + align256(part_o_floats(num_parts) * sizeof(float)));
+    auto map3 = [&](CUtensorMap* m, CUtensorMapDataType type, const void* base, cuuint64_t n, cuuint64_t row_bytes,
+                    cuuint64_t chunk_bytes, cuuint32_t box_rows, cuuint32_t box_chunks, CUtensorMapSwizzle sw) {
+        const cuuint64_t dim[3] = {64, n, 9}, stride[2] = {row_bytes, chunk_bytes};
+        const cuuint32_t box[3] = {64, box_rows, box_chunks};
+        return encode(m, type, 3, const_cast<void*>(base), dim, stride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    auto map2 = [&](CUtensorMap* m, CUtensorMapDataType type, void* base, cuuint64_t n, cuuint64_t size, cuuint32_t cols) {
+        const cuuint64_t dim[2] = {512, n}, stride[1] = {512 * size};
+        const cuuint32_t box[2] = {cols, 32};
+        return encode(m, type, 2, base, dim, stride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    bool ok;
+    if (kv_dtype == MLA_DTYPE_BF16) {
+        ok = map3(&k_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, k_cache, pool_rows, 1152, 128, 64, 9, CU_TENSOR_MAP_SWIZZLE_128B) &&
+             map3(&v_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, k_cache, pool_rows, 1152, 128, 64, 2, CU_TENSOR_MAP_SWIZZLE_128B);
+    } else {
+        ok = map3(&k_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, k_cache, pool_rows, 576, 64, 64, 9, CU_TENSOR_MAP_SWIZZLE_NONE);
+        v_map = k_map;   // the 8-bit path reads the partner's V through registers
+    }
+    ok = ok && map3(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, (cuuint64_t)rows, 1152, 128, 64, 5, CU_TENSOR_MAP_SWIZZLE_128B) &&
+         map2(&o_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, (cuuint64_t)rows, 2, 64) &&
+         map2(&ps_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, part_o, (cuuint64_t)num_parts * 2 * kTileRows, 4, 32);
+    if (!ok) return MLA_ERR_CUDA;
+
+    Params p;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.kv = static_cast<const uint8_t*>(k_cache);
+    p.block_table = block_table;
+    p.bt_stride = block_table_stride;
+    p.max_pages = max_pages;
+    p.cache_seqlens = cache_seqlens;
+    p.cu = cu_seqlens;
+    p.plan = chunk_plan;
+    p.bs = bs;
+    p.h = h_q;
+    p.num_tokens = num_tokens;
+    p.parts = num_parts;
+    p.num_pages = num_pages;
+    p.scale_log2 = softmax_scale * 1.4426950408889634f;
+    p.descale_q = descale_q;
+    p.descale_k = descale_k;
+    p.causal = causal;
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.lse = lse;
+    p.part_o = part_o;
+    p.part_lse = part_lse;
+    const uint64_t wait_budget = g_hook_wait_budget_ns.load(std::memory_order_relaxed);
+    p.wait_budget_ns = wait_budget ? wait_budget : mla::kWaitBudgetNs;
+    p.withhold_tile = g_hook_withhold_tile.load(std::memory_order_relaxed);
+
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * num_parts);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = mla::chunk::kSmemBytes;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    auto kernel = kv_dtype == MLA_DTYPE_BF16 ? mla_chunk_kernel<0>
+                  : (kv_dtype == MLA_DTYPE_FP8_E4M3 ? mla_chunk_kernel<1> : mla_chunk_kernel<2>);
+    if (cudaLaunchKernelEx(&cfg, kernel, k_map, v_map, q_map, o_map, ps_map, p) != cudaSuccess) return MLA_ERR_CUDA;
+    // the merge of the units that the plan cut: scheduled early, it waits on the device
+    cfg.gridDim = dim3(2 * num_parts);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.dynamicSmemBytes = 0;
+    return from_cuda(cudaLaunchKernelEx(&cfg, chunk_merge_kernel, chunk_plan, cu_seqlens, num_parts, bs, h_q, num_tokens,
+                                        (const float*)part_o, (const float*)part_lse, p.out, lse));
 }
 
 mla_status_t mla_set_test_hooks(uint64_t wait_budget_ns, int32_t withhold_tile, int32_t no_fold_in) {
