@@ -48,37 +48,43 @@ using decode::kQWarp0;
 using decode::kRaw8Off;
 using decode::kRescaleThreshold;
 using decode::kSoftmaxWarp0;
-using decode::kThreads;
 using decode::kTmemCols;
 using decode::kTmemO;
 using decode::kTmemQ;
 using decode::kTmemS;
 using decode::PageWindow;
 
+constexpr int kThreads = 512;          // 16 warps: 0, 3 K loads, 1 S issuer, 2 PV issuer (leader), 4..7
+                                       // and 12..15 softmax, 8..11 Q and partner V
+constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
+constexpr int kLoBoxes = kQLoChunks;   // a page's chunks 0..3 and 4..8 load, and free their slot, apart
+constexpr int kHiBoxes = kChunks - kLoBoxes;
+
 // Shared-memory map (offsets from the 1024-aligned base).
 constexpr int kOffQ = 0;                            // Q chunks 4..8
 constexpr int kOffK = kOffQ + kQHiBytes;
 constexpr int kOffP = kOffK + kKSlots * kKSlotBytes;
-constexpr int kOffX = kOffP + kPBytes;              // row-max exchange: 2 x 128 floats, row sums 128
-constexpr int kOffStage = kOffX + 2048;             // epilogue staging: 4 warps x 32 rows x 128 B
+constexpr int kOffX = kOffP + kPBytes;              // row-max exchange: 2 x 256 floats, row sums 256
+constexpr int kOffStage = kOffX + 3072;             // epilogue staging of warps 12..15: 32 rows x 128 B each
 constexpr int kOffPSig = kOffStage + 4 * 32 * 128;  // leader: landing words of the peer's signals
-constexpr int kOffBar = kOffPSig + 128;             // words: P 0..3, V 4..7, K 8, Q 9..12, S 16..19, O 20..23
+constexpr int kOffBar = kOffPSig + 256;             // words: P 0..7, V 8..11, K 12, 13, Q 14..17, S 18..25, O 26..33
 
 enum : int {
-    kBarKFull = 0,                      // leader (x slots): both CTAs' pages of the tile landed
-    kBarKEmpty = kBarKFull + kKSlots,   // both: the tile's PV finished (slot reusable)
-    kBarQKDone = kBarKEmpty + kKSlots,  // both: the tile's S MMAs finished reading the slot
-    kBarVFull = kBarQKDone + kKSlots,   // leader: the pair's partner V landed
-    kBarQFull = kBarVFull + kKSlots,    // leader: Q landed / was written
+    kBarKFull = 0,                      // leader (slot, half): both CTAs' chunks 0..3 / 4..8 landed
+    kBarKEmpty = kBarKFull + 2 * kKSlots,    // both (slot, half): the PV MMAs finished with chunks 0..3 / all
+    kBarQKDone = kBarKEmpty + 2 * kKSlots,   // both (slot): the tile's S MMAs finished reading the slot
+    kBarVFull = kBarQKDone + kKSlots,   // leader (slot, half): the pair's partner V of output block 0 / 1 landed
+    kBarQFull = kBarVFull + 2 * kKSlots,     // leader: Q landed / was written
     kBarQEmpty,                         // both: the unit's last S MMA finished (Q reusable)
     kBarSFull,                          // both (x2): S tile in tensor memory
-    kBarSFree = kBarSFull + 2,          // leader (x2): 8 softmax warps have read S
-    kBarPFull = kBarSFree + 2,          // leader: 8 softmax warps wrote P
+    kBarSFree = kBarSFull + 2,          // leader (x2): 16 softmax warps have read S
+    kBarPFull = kBarSFree + 2,          // leader: 16 softmax warps wrote P
     kBarPvDone,                         // both: the PV MMAs of a tile finished (P reusable)
     kBarOFull,                          // both: the unit's last PV finished
-    kBarOEmpty,                         // leader: 8 softmax warps read O out
-    kBarXchg,                           // local (x2): the 128 softmax threads posted row maxima
-    kBarLx = kBarXchg + 2,              // local: the 128 softmax threads posted row sums
+    kBarOEmpty,                         // leader: 16 softmax warps read O out
+    kBarXchg,                           // local (x2): the 8 softmax warps posted row maxima
+    kBarLx = kBarXchg + 2,              // local: the 8 softmax warps posted row sums
     kBarVTail,                          // local: the partner V of a tile with a cut page landed
     kBarKRaw,                           // local (x2), 8-bit cache: this CTA's page landed
     kNumBars = kBarKRaw + kKSlots
@@ -225,8 +231,8 @@ __device__ __forceinline__ void clear_v_rows(uint32_t slot, int c, int valid, in
 // kKv: the cache's element type, 0 bf16, 1 e4m3, 2 e5m2 (8-bit caches are widened to f16).
 template <int kKv>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                 const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap o_map,
+mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap klo_map,
+                 const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap o_map,
                  const __grid_constant__ CUtensorMap ps_map, const __grid_constant__ Params p) {
     constexpr bool kFp8 = kKv != 0;
     constexpr bool kE5M2 = kKv == 2;
@@ -246,10 +252,12 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kKSlots; ++s) {
-            mbar_init(bar(kBarKFull + s), 1);
-            mbar_init(bar(kBarKEmpty + s), 1);
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(bar(kBarKFull + 2 * s + j), 1);
+                mbar_init(bar(kBarKEmpty + 2 * s + j), 1);
+                mbar_init(bar(kBarVFull + 2 * s + j), kFp8 ? 4 : 1);
+            }
             mbar_init(bar(kBarQKDone + s), 1);
-            mbar_init(bar(kBarVFull + s), kFp8 ? 4 : 1);
             mbar_init(bar(kBarKRaw + s), 1);
         }
         // the Q TMA (bf16 cache) and the 4 warps that write Q
@@ -257,15 +265,14 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
         mbar_init(bar(kBarQEmpty), 1);
         for (int j = 0; j < 2; ++j) {
             mbar_init(bar(kBarSFull + j), 1);
-            mbar_init(bar(kBarSFree + j), 4);
+            mbar_init(bar(kBarSFree + j), kSoftmaxWarps);
+            mbar_init(bar(kBarXchg + j), kSoftmaxWarps);
         }
-        mbar_init(bar(kBarPFull), 4);
+        mbar_init(bar(kBarPFull), kSoftmaxWarps);
         mbar_init(bar(kBarPvDone), 1);
         mbar_init(bar(kBarOFull), 1);
-        mbar_init(bar(kBarOEmpty), 4);
-        mbar_init(bar(kBarXchg), 128);
-        mbar_init(bar(kBarXchg + 1), 128);
-        mbar_init(bar(kBarLx), 128);
+        mbar_init(bar(kBarOEmpty), kSoftmaxWarps);
+        mbar_init(bar(kBarLx), kSoftmaxWarps);
         mbar_init(bar(kBarVTail), 1);
         *abort_flag = 0;
         fence_mbarrier_init_cluster();
@@ -276,6 +283,7 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
     }
     if (warp == 0 && lane == 0) {
         prefetch_tensormap(&k_map);
+        prefetch_tensormap(&klo_map);
         prefetch_tensormap(&v_map);
         prefetch_tensormap(&q_map);
         prefetch_tensormap(&o_map);
@@ -337,15 +345,26 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 const uint32_t slot = sbase + kOffK + s * kKSlotBytes;
                 const bool withhold = leader && (int)g == p.withhold_tile;
                 if (lane == 0) {
-                    ok = mbar_wait_bounded(bar(kBarKEmpty + s), ((g >> 1) & 1u) ^ 1u, actl);
-                    if (ok && !withhold) {
-                        if constexpr (kFp8) {
+                    const uint32_t free = ((g >> 1) & 1u) ^ 1u;
+                    if constexpr (kFp8) {
+                        // the raw page lies in the slot's back half
+                        ok = mbar_wait_bounded(bar(kBarKEmpty + 2 * s + 1), free, actl);
+                        if (ok && !withhold) {
                             mbar_arrive_expect_tx(bar(kBarKRaw + s), kPage8Bytes);
                             tma_load_3d(slot + kRaw8Off, &k_map, bar(kBarKRaw + s), 0, row, 0);
-                        } else {
-                            const uint32_t kf = bar(kBarKFull + s);
-                            if (leader) mbar_arrive_expect_tx(kf, 2 * kChunks * kBox);
-                            tma_load_3d_pair(slot, &k_map, map_to_cta(kf, 0), 0, row, 0);
+                        }
+                    } else {
+                        ok = mbar_wait_bounded(bar(kBarKEmpty + 2 * s), free, actl);
+                        if (ok && !withhold) {
+                            const uint32_t kf = bar(kBarKFull + 2 * s);
+                            if (leader) mbar_arrive_expect_tx(kf, 2 * kLoBoxes * kBox);
+                            tma_load_3d_pair(slot, &klo_map, map_to_cta(kf, 0), 0, row, 0);
+                        }
+                        ok = ok && mbar_wait_bounded(bar(kBarKEmpty + 2 * s + 1), free, actl);
+                        if (ok && !withhold) {
+                            const uint32_t kf = bar(kBarKFull + 2 * s + 1);
+                            if (leader) mbar_arrive_expect_tx(kf, 2 * kHiBoxes * kBox);
+                            tma_load_3d_pair(slot + kLoBoxes * kBox, &k_map, map_to_cta(kf, 0), 0, row, kLoBoxes);
                         }
                     }
                 }
@@ -361,15 +380,18 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                     }
                     const int valid = u.L - blk * kPage;
 #pragma unroll 1
-                    for (int c = 0; c < kChunks; ++c)
+                    for (int c = 0; c < kChunks; ++c) {
                         widen_chunk_rows<kE5M2>(slot + kRaw8Off + c * kChunk8, slot + c * kBox, lane, valid);
-                    fence_proxy_async_smem();
-                    signal_leader(kBarKFull + s, 8);
+                        if (c == kLoBoxes - 1 || c == kChunks - 1) {
+                            fence_proxy_async_smem();
+                            signal_leader(kBarKFull + 2 * s + (c == kChunks - 1), 12 + (c == kChunks - 1));
+                        }
+                    }
                 }
             }
         }
         drain_on_abort();
-    } else if (warp >= kQWarp0) {
+    } else if (warp >= kQWarp0 && warp < kQWarp0 + 4) {
         // ------------------------------------------------------------ Q and partner V
         const int quarter = warp & 3;
         const int qt = threadIdx.x - kQWarp0 * 32;          // 0..127
@@ -392,12 +414,13 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             }
             const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)u.row0 + rtile) * kDqk);
             const bool have = rtile < u.nrows;
-            {
-                uint4 v[32];   // the row's columns [0, 256): all loads in flight at once
 #pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = have ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+            for (int hb = 0; hb < 2; ++hb) {
+                uint4 v[16];   // 128 of the row's columns [0, 256): their loads in flight at once
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int k = 0; k < 16; ++k) v[k] = have ? __ldg(src + 16 * hb + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
                     uint32_t w[16];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -410,7 +433,7 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
 #pragma unroll
                         for (int k = 0; k < 16; ++k) w[k] = decode::bf16x2_to_f16x2(w[k], q_range);
                     }
-                    tmem_st16(tmem + lane_off + kTmemQ + 16u * c, w);
+                    tmem_st16(tmem + lane_off + kTmemQ + 64u * hb + 16u * c, w);
                 }
             }
             if constexpr (kFp8) {
@@ -434,7 +457,7 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             }
             tc_wait_st();
             tc_fence_before();
-            signal_leader(kBarQFull, 9 + quarter);
+            signal_leader(kBarQFull, 14 + quarter);
             ++uq;
             // ---- partner V of each tile of the unit
             const int32_t* bt_row = p.block_table + (int64_t)u.b * p.bt_stride;
@@ -456,18 +479,16 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                             ok = mbar_wait_bounded(bar(kBarQKDone + s), (g >> 1) & 1u, actl);
                             if (ok) {
                                 const int32_t row = pg >= 0 ? pg * kPage : (int32_t)(p.num_pages * kPage);
-                                if (cut)
-                                    mbar_arrive_expect_tx(bar(kBarVTail), 2 * 2 * kBox);
-                                else if (leader)
-                                    mbar_arrive_expect_tx(bar(kBarVFull + s), 2 * 2 * 2 * kBox);
+                                if (cut) mbar_arrive_expect_tx(bar(kBarVTail), 2 * 2 * kBox);
 #pragma unroll
                                 for (int nn = 0; nn < 2; ++nn) {
+                                    const uint32_t vf = bar(kBarVFull + 2 * s + nn);
+                                    if (!cut && leader) mbar_arrive_expect_tx(vf, 2 * 2 * kBox);
                                     const uint32_t dst = slot + (4 * nn + 2 * (1 - (int)rank)) * kBox;
                                     if (cut)
                                         tma_load_3d(dst, &v_map, bar(kBarVTail), 0, row, 4 * nn + 2 * (int)rank);
                                     else
-                                        tma_load_3d_pair(dst, &v_map, map_to_cta(bar(kBarVFull + s), 0), 0, row,
-                                                         4 * nn + 2 * (int)rank);
+                                        tma_load_3d_pair(dst, &v_map, map_to_cta(vf, 0), 0, row, 4 * nn + 2 * (int)rank);
                                 }
                             }
                         }
@@ -478,7 +499,8 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                             ok = __all_sync(0xffffffffu, landed);
                             if (valid < kPage) clear_v_rows(slot, 2 * (1 - (int)rank), valid, lane);
                             fence_proxy_async_smem();
-                            signal_leader(kBarVFull + s, 4);
+                            signal_leader(kBarVFull + 2 * s, 8);
+                            signal_leader(kBarVFull + 2 * s + 1, 9);
                             ++ntail;
                         }
                         if (!ok) {
@@ -516,136 +538,129 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                         st_shared_v4u(r + 16u * ((2u * q4 + 1u) ^ sw), fp8x2_to_f16x2<kE5M2>(v[j].z),
                                       fp8x2_to_f16x2<kE5M2>(v[j].z >> 16), fp8x2_to_f16x2<kE5M2>(v[j].w),
                                       fp8x2_to_f16x2<kE5M2>(v[j].w >> 16));
+                        if (j == 3 || j == 7) {   // an output block's two chunks are in place
+                            fence_proxy_async_smem();
+                            signal_leader(kBarVFull + 2 * s + (j >> 2), 8 + quarter);
+                        }
                     }
-                    fence_proxy_async_smem();
-                    signal_leader(kBarVFull + s, 4 + quarter);
                 }
             }
         }
         if (!kFp8 && quarter == 3) drain_on_abort();
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer (leader)
-        // Two cursors walk the same tiles: S(t) = Q K^T and O += P(t) V(t); whichever is ready goes
-        // first, PV before S.  The whole warp walks, an elected lane issues each MMA.
+        // ------------------------------------------------------------ S issuer (leader)
+        // A warp each for S and PV, so that neither waits behind the other's barriers; the whole
+        // warp walks the tiles, an elected lane issues each MMA.
         if (leader) {
-            auto poll = [](uint32_t b, uint32_t parity) -> bool {
-                return __all_sync(0xffffffffu, mbar_test_wait(b, parity));
+            uint32_t g = 0, uq = 0;
+            bool alive = true;
+            auto wait = [&](int b, uint32_t parity) -> bool {
+                return __all_sync(0xffffffffu, mbar_wait_bounded(bar(b), parity, actl));
             };
-            struct Cursor {
-                UnitIter it;
-                int n, i;
-                uint32_t g, uq;
-                bool valid;
-                __device__ void next_unit(const Params& pp) {
-                    Unit v;
-                    valid = false;
-                    while (it.next(pp, v)) {
-                        n = v.tiles();
-                        if (n > 0) {
-                            i = 0;
-                            valid = true;
-                            return;
-                        }
-                    }
-                }
-                __device__ void step(const Params& pp) {
-                    ++g;
-                    if (++i == n) {
-                        ++uq;
-                        next_unit(pp);
-                    }
-                }
-            };
-            Cursor cq, cp;
-            cq.it = iter;
-            cq.g = 0;
-            cq.uq = 0;
-            cq.n = cq.i = 0;
-            cq.next_unit(p);
-            cp = cq;
-            uint64_t t_idle = global_timer_ns();
-            while (cq.valid || cp.valid) {
-                bool did = false;
-                if (cp.valid && cp.g < cq.g) {
-                    const int s = (int)(cp.g & 1u);
-                    const bool first = cp.i == 0;
-                    if (poll(bar(kBarPFull), cp.g & 1u) && poll(bar(kBarVFull + s), (cp.g >> 1) & 1u) &&
-                        (!first || cp.uq == 0 || poll(bar(kBarOEmpty), (cp.uq - 1) & 1u))) {
-                        tc_fence_after();
-                        const uint32_t pbuf = sbase + kOffP;
-                        const uint32_t slot = sbase + kOffK + s * kKSlotBytes;
-#pragma unroll
-                        for (int nn = 0; nn < 2; ++nn)
-#pragma unroll
-                            for (int pp = 0; pp < 2; ++pp)
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk)
-                                    mma_pair_ss(tmem + kTmemO + 128u * nn,
-                                                smem_desc_sw128(pbuf + pp * kBox + 32u * kk, 16, 1024),
-                                                smem_desc_sw128(slot + (4 * nn + 2 * pp) * kBox + 2048u * kk, kBox, 1024),
-                                                kFp8 ? kIdescPV16 : kIdescPV, (first && pp == 0 && kk == 0) ? 0u : 1u);
-                        tc_commit_pair(bar(kBarKEmpty + s));
-                        tc_commit_pair(bar(kBarPvDone));
-                        if (cp.i == cp.n - 1) tc_commit_pair(bar(kBarOFull));
-                        cp.step(p);
-                        did = true;
-                    }
-                }
-                if (!did && cq.valid) {
-                    const int s = (int)(cq.g & 1u);
-                    const uint32_t sb = cq.g & 1u;
-                    if ((cq.i != 0 || poll(bar(kBarQFull), cq.uq & 1u)) &&
-                        (cq.g < 2 || poll(bar(kBarSFree + sb), ((cq.g >> 1) & 1u) ^ 1u)) &&
-                        poll(bar(kBarKFull + s), (cq.g >> 1) & 1u)) {
-                        tc_fence_after();
-                        const uint32_t slot = sbase + kOffK + s * kKSlotBytes;
-                        const uint32_t d = tmem + kTmemS + 64u * sb;
-#pragma unroll
-                        for (int c = 0; c < kChunks; ++c) {
-                            if (c < kQLoChunks) {
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk)
-                                    mma_pair_ts(d, tmem + kTmemQ + 32u * c + 8u * kk,
-                                                smem_desc_sw128(slot + c * kBox + 32u * kk, 16, 1024),
-                                                kFp8 ? kIdescQK16 : kIdescQK, (c | kk) ? 1u : 0u);
-                            } else {
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk)
-                                    mma_pair_ss(d, smem_desc_sw128(sbase + kOffQ + (c - kQLoChunks) * kBox + 32u * kk, 16, 1024),
-                                                smem_desc_sw128(slot + c * kBox + 32u * kk, 16, 1024),
-                                                kFp8 ? kIdescQK16 : kIdescQK, 1u);
-                            }
-                        }
-                        tc_commit_pair(bar(kBarQKDone + s));
-                        tc_commit_pair(bar(kBarSFull + sb));
-                        if (cq.i == cq.n - 1) tc_commit_pair(bar(kBarQEmpty));
-                        cq.step(p);
-                        did = true;
-                    }
-                }
-                if (did) {
-                    t_idle = global_timer_ns();
-                } else {
-                    if (*abort_flag) break;
-                    if (global_timer_ns() - t_idle > actl.budget_ns) {
-                        if (lane == 0) raise_abort(actl);
+            Unit u;
+            while (alive && iter.next(p, u)) {
+                const int n = u.tiles();
+                if (n <= 0) continue;
+                if (!wait(kBarQFull, uq & 1u)) break;
+                for (int i = 0; i < n; ++i, ++g) {
+                    const int s = (int)(g & 1u);
+                    const uint32_t slot = sbase + kOffK + s * kKSlotBytes;
+                    const uint32_t d = tmem + kTmemS + 64u * (g & 1u);
+                    if ((g >= 2 && !wait(kBarSFree + s, ((g >> 1) & 1u) ^ 1u)) || !wait(kBarKFull + 2 * s, (g >> 1) & 1u)) {
+                        alive = false;
                         break;
                     }
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < kQLoChunks; ++c)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_pair_ts(d, tmem + kTmemQ + 32u * c + 8u * kk, smem_desc_sw128(slot + c * kBox + 32u * kk, 16, 1024),
+                                        kFp8 ? kIdescQK16 : kIdescQK, (c | kk) ? 1u : 0u);
+                    if (!wait(kBarKFull + 2 * s + 1, (g >> 1) & 1u)) {
+                        alive = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = kQLoChunks; c < kChunks; ++c)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_pair_ss(d, smem_desc_sw128(sbase + kOffQ + (c - kQLoChunks) * kBox + 32u * kk, 16, 1024),
+                                        smem_desc_sw128(slot + c * kBox + 32u * kk, 16, 1024), kFp8 ? kIdescQK16 : kIdescQK, 1u);
+                    tc_commit_pair(bar(kBarQKDone + s));
+                    tc_commit_pair(bar(kBarSFull + s));
+                    if (i == n - 1) tc_commit_pair(bar(kBarQEmpty));
                 }
+                ++uq;
             }
         }
-    } else if (warp >= kSoftmaxWarp0 && warp < kSoftmaxWarp0 + 4) {
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ PV issuer (leader)
+        // Output block 0 (slot chunks 0..3) before block 1 (4..7): each half of the slot goes back to
+        // the K loads as soon as its block is done.
+        if (leader) {
+            uint32_t g = 0, uq = 0;
+            bool alive = true;
+            auto wait = [&](int b, uint32_t parity) -> bool {
+                return __all_sync(0xffffffffu, mbar_wait_bounded(bar(b), parity, actl));
+            };
+            Unit u;
+            while (alive && iter.next(p, u)) {
+                const int n = u.tiles();
+                if (n <= 0) continue;
+                if (uq > 0 && !wait(kBarOEmpty, (uq - 1) & 1u)) break;
+                for (int i = 0; i < n; ++i, ++g) {
+                    const int s = (int)(g & 1u);
+                    const uint32_t slot = sbase + kOffK + s * kKSlotBytes;
+                    if (!wait(kBarPFull, g & 1u)) {
+                        alive = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int nn = 0; nn < 2; ++nn) {
+                        if (!wait(kBarVFull + 2 * s + nn, (g >> 1) & 1u)) {
+                            alive = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll
+                        for (int pp = 0; pp < 2; ++pp)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_pair_ss(tmem + kTmemO + 128u * nn,
+                                            smem_desc_sw128(sbase + kOffP + pp * kBox + 32u * kk, 16, 1024),
+                                            smem_desc_sw128(slot + (4 * nn + 2 * pp) * kBox + 2048u * kk, kBox, 1024),
+                                            kFp8 ? kIdescPV16 : kIdescPV, (i == 0 && pp == 0 && kk == 0) ? 0u : 1u);
+                        tc_commit_pair(bar(kBarKEmpty + 2 * s + nn));
+                    }
+                    if (!alive) break;
+                    tc_commit_pair(bar(kBarPvDone));
+                    if (i == n - 1) tc_commit_pair(bar(kBarOFull));
+                }
+                ++uq;
+            }
+        }
+    } else {
         // ------------------------------------------------------------ softmax / epilogue
-        const int t = threadIdx.x - kSoftmaxWarp0 * 32;       // TMEM lane
+        // Two warps per tensor-memory lane quarter (4..7 and 12..15): a thread has 32 of a row's 128
+        // keys, and 128 of its CTA row's 256 tensor-memory columns of O.
+        const int quarter = warp & 3, sub = warp >> 3;
+        const int t = 32 * quarter + lane;                    // TMEM lane
         const int rloc = t & 63;                              // row within this CTA's 64
-        const int half = t >> 6;                              // token half of each tile
-        const uint32_t lane_off = (uint32_t)((warp - kSoftmaxWarp0) * 32) << 16;
+        const int half = t >> 6;                              // key half (page) of each tile
+        const int sw8 = quarter + 4 * sub;                    // softmax warp 0..7
+        const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
         const int rtile = kCtaRows * (int)rank + rloc;        // row of the unit's tile
         const float dq = p.descale_q ? *p.descale_q : 1.0f;
         const float dk = p.descale_k ? *p.descale_k : 1.0f;
         const float sl2 = p.scale_log2 * dq * dk;
-        float* xmax = reinterpret_cast<float*>(smem + kOffX);  // [2][128] row maxima, [128] sums
+        float* xmax = reinterpret_cast<float*>(smem + kOffX);  // [2][256] row maxima, [256] sums
         const uint32_t swz = (uint32_t)(rloc & 7);
+        auto post = [&](int b) {   // this warp's shared-memory posts are done
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(b));
+        };
 
         uint32_t g = 0, uq = 0;
         bool alive = true;
@@ -656,9 +671,9 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             if (n <= 0) {
                 // no key at all: o = 0, lse = -inf
                 if (row_valid) {
-                    __nv_bfloat16* row_out = p.out + ((int64_t)u.row0 + rtile) * kDv + 256 * half;
-                    for (int c = 0; c < 32; ++c) reinterpret_cast<uint4*>(row_out)[c] = make_uint4(0, 0, 0, 0);
-                    if (half == 0) p.lse[(int64_t)u.row0 + rtile] = -INFINITY;
+                    __nv_bfloat16* row_out = p.out + ((int64_t)u.row0 + rtile) * kDv + 256 * half + 128 * sub;
+                    for (int c = 0; c < 16; ++c) reinterpret_cast<uint4*>(row_out)[c] = make_uint4(0, 0, 0, 0);
+                    if (half == 0 && sub == 0) p.lse[(int64_t)u.row0 + rtile] = -INFINITY;
                 }
                 continue;
             }
@@ -668,7 +683,7 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 lim = l < u.L ? (int)l : u.L;
             }
             if (lim > u.kb1 * kPage) lim = u.kb1 * kPage;   // keys of this piece (and of the table) only
-            float m_run = -INFINITY, l_half = 0.f;
+            float m_run = -INFINITY, l_part = 0.f;
             for (int i = 0; i < n; ++i, ++g) {
                 const uint32_t sb = g & 1u;
                 if (!mbar_wait_bounded(bar(kBarSFull + sb), (g >> 1) & 1u, actl)) {
@@ -676,60 +691,64 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                     break;
                 }
                 tc_fence_after();
-                float s[64];
+                float s[32];
                 {
-                    uint32_t raw[4][16];
+                    uint32_t raw[2][16];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tmem_ld16(tmem + lane_off + kTmemS + 64u * sb + 16u * c, raw[c]);
+                    for (int c = 0; c < 2; ++c)
+                        tmem_ld16(tmem + lane_off + kTmemS + 64u * sb + 32u * sub + 16u * c, raw[c]);
                     tc_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int k = 0; k < 16; ++k) s[16 * c + k] = __uint_as_float(raw[c][k]);
                 }
                 tc_fence_before();
-                signal_leader(kBarSFree + sb, 16 + (warp - kSoftmaxWarp0));
-                // scale to log2 units, mask the keys at or past the limit, this half's maximum
-                const int kbase = (u.t0 + i) * kTileKeys + kPage * half;
+                signal_leader(kBarSFree + sb, 18 + sw8);
+                // scale to log2 units, mask the keys at or past the limit, these keys' maximum
+                const int kbase = (u.t0 + i) * kTileKeys + kPage * half + 32 * sub;
 #pragma unroll
-                for (int j = 0; j < 64; j += 2) mul2(s[j], s[j + 1], sl2);
-                if (kbase + 64 > lim) {
+                for (int j = 0; j < 32; j += 2) mul2(s[j], s[j + 1], sl2);
+                if (kbase + 32 > lim) {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j)
+                    for (int j = 0; j < 32; ++j)
                         if (kbase + j >= lim) s[j] = -INFINITY;
                 }
                 float hmax;
                 {
                     float m0 = fmaxf(s[0], s[1]), m1 = fmaxf(s[2], s[3]);
 #pragma unroll
-                    for (int j = 4; j < 64; j += 4) {
+                    for (int j = 4; j < 32; j += 4) {
                         m0 = fmax3(m0, s[j], s[j + 1]);
                         m1 = fmax3(m1, s[j + 2], s[j + 3]);
                     }
                     hmax = fmaxf(m0, m1);
                 }
-                // partner thread t ^ 64 holds the other 64 tokens of this row
-                xmax[sb * 128 + t] = hmax;
-                mbar_arrive(bar(kBarXchg + sb));
+                // three other threads hold the row's other keys
+                xmax[sb * kSoftmaxThreads + 128 * sub + t] = hmax;
+                post(kBarXchg + sb);
                 if (!mbar_wait_bounded(bar(kBarXchg + sb), (g >> 1) & 1u, actl)) {
                     alive = false;
                     break;
                 }
-                const float tmax = fmaxf(hmax, xmax[sb * 128 + (t ^ 64)]);
+                float tmax;
+                {
+                    const float* x = xmax + sb * kSoftmaxThreads + rloc;
+                    tmax = fmaxf(fmaxf(x[0], x[64]), fmaxf(x[128], x[192]));
+                }
                 const float m_new = fmaxf(m_run, tmax);
                 const bool rescale = m_new > m_run + kRescaleThreshold;
                 float factor = 1.f;
                 if (rescale) {
                     factor = fast_exp2(m_run - m_new);  // 0 when m_run = -inf
-                    l_half *= factor;
+                    l_part *= factor;
                     m_run = m_new;
                 }
-                // P packed in pairs into s[0..31]; zeros while every key so far is masked
+                // P packed in pairs into s[0..15]; zeros while every key so far is masked
                 if (m_run != -INFINITY) {
                     float ps0 = 0.f, ps1 = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
+                    for (int j = 0; j < 16; ++j) {
                         float p0 = s[2 * j], p1 = s[2 * j + 1];
                         sub2(p0, p1, m_run);
                         p0 = fast_exp2(p0);
@@ -737,10 +756,10 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                         add2(ps0, ps1, p0, p1);
                         s[j] = __uint_as_float(kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1));
                     }
-                    l_half += ps0 + ps1;
+                    l_part += ps0 + ps1;
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) s[j] = 0.f;
+                    for (int j = 0; j < 16; ++j) s[j] = 0.f;
                 }
                 // the P buffer is free, and O holds every PV up to tile g - 1, once PV(g - 1) is done
                 if (g >= 1 && !mbar_wait_bounded(bar(kBarPvDone), (g - 1) & 1u, actl)) {
@@ -750,14 +769,14 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 if (i > 0 && __any_sync(0xffffffffu, rescale)) {
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < 16; ++c) {
+                    for (int c = 0; c < 8; ++c) {
                         uint32_t raw[16];
-                        tmem_ld16(tmem + lane_off + kTmemO + 16u * c, raw);
+                        tmem_ld16(tmem + lane_off + kTmemO + 128u * sub + 16u * c, raw);
                         tc_wait_ld();
 #pragma unroll
                         for (int k = 0; k < 16; ++k)
                             raw[k] = __float_as_uint(__uint_as_float(raw[k]) * factor);
-                        tmem_st16(tmem + lane_off + kTmemO + 16u * c, raw);
+                        tmem_st16(tmem + lane_off + kTmemO + 128u * sub + 16u * c, raw);
                     }
                     tc_wait_st();
                     tc_fence_before();
@@ -766,50 +785,56 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 {
                     const uint32_t prow = sbase + kOffP + half * kBox + rloc * 128u;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        st_shared_v4u(prow + ((c ^ swz) << 4), __float_as_uint(s[4 * c]),
+                    for (int c = 0; c < 4; ++c)
+                        st_shared_v4u(prow + (((4u * sub + c) ^ swz) << 4), __float_as_uint(s[4 * c]),
                                       __float_as_uint(s[4 * c + 1]), __float_as_uint(s[4 * c + 2]),
                                       __float_as_uint(s[4 * c + 3]));
                 }
                 fence_proxy_async_smem();
-                signal_leader(kBarPFull, warp - kSoftmaxWarp0);
+                signal_leader(kBarPFull, sw8);
             }
             if (!alive) break;
             // ---- epilogue of the unit: o (or the piece's fp32 partial, normalised) and lse
             if (!mbar_wait_bounded(bar(kBarOFull), uq & 1u, actl)) break;
             tc_fence_after();
-            xmax[256 + t] = l_half;
-            mbar_arrive(bar(kBarLx));
+            xmax[2 * kSoftmaxThreads + 128 * sub + t] = l_part;
+            post(kBarLx);
             if (!mbar_wait_bounded(bar(kBarLx), uq & 1u, actl)) break;
-            const float l_run = l_half + xmax[256 + (t ^ 64)];
+            float l_run;
+            {
+                const float* x = xmax + 2 * kSoftmaxThreads + rloc;
+                l_run = (x[0] + x[64]) + (x[128] + x[192]);
+            }
             const float inv = l_run > 0.f ? dk / l_run : 0.f;
             const float lse_val = l_run > 0.f ? (m_run + __log2f(l_run)) * 0.69314718055994531f : -INFINITY;
             const bool direct = u.slot < 0;
             {
-                // 64 tensor-memory columns a step, staged 32 rows x 128 bytes at a time (128-byte
-                // swizzle): the warp's own 4 KB and its 4 KB of the P buffer, idle now, alternate.
-                const uint32_t stage_a = sbase + kOffStage + (uint32_t)(warp - kSoftmaxWarp0) * 4096u;
-                const uint32_t stage_b = sbase + kOffP + (uint32_t)(warp - kSoftmaxWarp0) * 4096u;
+                // Each warp has 32 rows x 128 tensor-memory columns (output block `sub`), 64 a step,
+                // staged 32 rows x 128 bytes at a time (128-byte swizzle) in 4 KB of its own: of the
+                // P buffer (idle: the next P is written after the next tile's row-max exchange, in
+                // which every softmax warp takes part) or of the staging area.
+                const uint32_t stage = sbase + (sub ? kOffStage : kOffP) + (uint32_t)quarter * 4096u;
                 uint32_t npass = 0;
-                const int r0 = kCtaRows * (int)rank + 32 * ((warp - kSoftmaxWarp0) & 1);   // the warp's first row
+                const int r0 = kCtaRows * (int)rank + 32 * (quarter & 1);   // the warp's first row
                 const int rows = min(32, u.nrows - r0);   // of its rows in the unit (<= 0: none)
 #pragma unroll 1
-                for (int st = 0; st < 4; ++st) {
+                for (int st = 0; st < 2; ++st) {
                     uint32_t raw[64];
-                    tmem_ld16(tmem + lane_off + kTmemO + 64u * st, *reinterpret_cast<uint32_t(*)[16]>(raw));
-                    tmem_ld16(tmem + lane_off + kTmemO + 64u * st + 16u, *reinterpret_cast<uint32_t(*)[16]>(raw + 16));
-                    tmem_ld16(tmem + lane_off + kTmemO + 64u * st + 32u, *reinterpret_cast<uint32_t(*)[16]>(raw + 32));
-                    tmem_ld16(tmem + lane_off + kTmemO + 64u * st + 48u, *reinterpret_cast<uint32_t(*)[16]>(raw + 48));
+                    const uint32_t src = tmem + lane_off + kTmemO + 128u * sub + 64u * st;
+                    tmem_ld16(src, *reinterpret_cast<uint32_t(*)[16]>(raw));
+                    tmem_ld16(src + 16u, *reinterpret_cast<uint32_t(*)[16]>(raw + 16));
+                    tmem_ld16(src + 32u, *reinterpret_cast<uint32_t(*)[16]>(raw + 32));
+                    tmem_ld16(src + 48u, *reinterpret_cast<uint32_t(*)[16]>(raw + 48));
                     tc_wait_ld();
-                    if (st == 3) {
+                    if (st == 1) {
                         tc_fence_before();
-                        signal_leader(kBarOEmpty, 20 + (warp - kSoftmaxWarp0));   // O is free for the next unit
+                        signal_leader(kBarOEmpty, 26 + sw8);   // O is free for the next unit
                     }
 #pragma unroll
                     for (int pass = 0; pass < 2; ++pass) {
                         if (direct && pass == 1) break;
                         uint32_t w[32];
-                        int col = 256 * (st >> 1) + 128 * half + 64 * (st & 1);
+                        int col = 256 * sub + 128 * half + 64 * st;
                         if (direct) {
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
@@ -819,8 +844,7 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                             for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(__uint_as_float(raw[32 * pass + k]) * inv);
                             col += 32 * pass;
                         }
-                        const uint32_t stage = (npass & 1u) ? stage_b : stage_a;
-                        if (lane == 0 && npass >= 2) bulk_wait_read<1>();
+                        if (lane == 0 && npass >= 1) bulk_wait_read<0>();
                         __syncwarp();
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
@@ -851,7 +875,7 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             }
             if (lane == 0) bulk_wait_read<0>();   // the staging (and the P buffer) free again
             __syncwarp();
-            if (half == 0) {
+            if (half == 0 && sub == 0) {
                 if (!direct)
                     st_global_f32_hint(p.part_lse + (int64_t)u.slot * kTileRows + rtile, row_valid ? lse_val : -INFINITY, part_pol);
                 else if (row_valid)

@@ -720,11 +720,12 @@ mla_status_t mla_chunk_paged(const void* q, int32_t q_dtype, int32_t num_tokens,
     EncodeTiledFn encode = encode_tiled();
     if (!encode) return MLA_ERR_CUDA;
 
-    // Tensor maps, as mla_decode_paged's: K pages as nine 64-column chunks, V as two-chunk boxes, q
+    // Tensor maps, as mla_decode_paged's: K pages as 64-column chunks (bf16: 0..3 and
+    // 4..8 apart; 8-bit: all nine), V as two-chunk boxes, q
     // rows (64 columns, rows, 9 chunks) in boxes of 64 rows x columns [256, 576), o rows and partial
     // rows as 32-row x 128-byte boxes (128-byte swizzle).
     const int32_t rows = num_tokens * h_q;
-    CUtensorMap k_map, v_map, q_map, o_map, ps_map;
+    CUtensorMap k_map, klo_map, v_map, q_map, o_map, ps_map;
     const cuuint64_t pool_rows = (cuuint64_t)num_pages * 64;
     const cuuint32_t es[3] = {1, 1, 1};
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -745,11 +746,12 @@ mla_status_t mla_chunk_paged(const void* q, int32_t q_dtype, int32_t num_tokens,
     };
     bool ok;
     if (kv_dtype == MLA_DTYPE_BF16) {
-        ok = map3(&k_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, k_cache, pool_rows, 1152, 128, 64, 9, CU_TENSOR_MAP_SWIZZLE_128B) &&
+        ok = map3(&k_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, k_cache, pool_rows, 1152, 128, 64, kHiBoxes, CU_TENSOR_MAP_SWIZZLE_128B) &&
+             map3(&klo_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, k_cache, pool_rows, 1152, 128, 64, kLoBoxes, CU_TENSOR_MAP_SWIZZLE_128B) &&
              map3(&v_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, k_cache, pool_rows, 1152, 128, 64, 2, CU_TENSOR_MAP_SWIZZLE_128B);
     } else {
         ok = map3(&k_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, k_cache, pool_rows, 576, 64, 64, 9, CU_TENSOR_MAP_SWIZZLE_NONE);
-        v_map = k_map;   // the 8-bit path reads the partner's V through registers
+        klo_map = v_map = k_map;   // the 8-bit path loads whole pages, and the partner's V through registers
     }
     ok = ok && map3(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, (cuuint64_t)rows, 1152, 128, 64, 5, CU_TENSOR_MAP_SWIZZLE_128B) &&
          map2(&o_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, (cuuint64_t)rows, 2, 64) &&
@@ -794,7 +796,7 @@ mla_status_t mla_chunk_paged(const void* q, int32_t q_dtype, int32_t num_tokens,
     cfg.numAttrs = 1;
     auto kernel = kv_dtype == MLA_DTYPE_BF16 ? mla_chunk_kernel<0>
                   : (kv_dtype == MLA_DTYPE_FP8_E4M3 ? mla_chunk_kernel<1> : mla_chunk_kernel<2>);
-    if (cudaLaunchKernelEx(&cfg, kernel, k_map, v_map, q_map, o_map, ps_map, p) != cudaSuccess) return MLA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, k_map, klo_map, v_map, q_map, o_map, ps_map, p) != cudaSuccess) return MLA_ERR_CUDA;
     // the merge of the units that the plan cut: scheduled early, it waits on the device
     cfg.gridDim = dim3(2 * num_parts);
     cfg.blockDim = dim3(kMergeThreads);
