@@ -54,8 +54,9 @@ using decode::kTmemQ;
 using decode::kTmemS;
 using decode::PageWindow;
 
-constexpr int kThreads = 512;          // 16 warps: 0, 3 K loads, 1 S issuer, 2 PV issuer (leader), 4..7
-                                       // and 12..15 softmax, 8..11 Q and partner V
+constexpr int kThreads = 512;          // 16 warps: 0 K loads, 1 S issuer, 2 PV issuer (leader), 3 partner V
+                                       // (8-bit cache: K of odd tiles), 4..7 and 12..15 softmax, 8..11 Q
+                                       // (8-bit cache: and partner V)
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
 constexpr int kLoBoxes = kQLoChunks;   // a page's chunks 0..3 and 4..8 load, and free their slot, apart
@@ -325,8 +326,9 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
         }
     };
 
-    if (warp == 0 || warp == 3) {
-        // ------------------------------------------------------------ K producers
+    if (warp == 0 || (kFp8 && warp == 3)) {
+        // ------------------------------------------------------------ K loads
+        // (8-bit cache: two warps take alternate tiles, and widen them)
         const uint32_t mine = warp == 3 ? 1u : 0u;
         uint32_t g = 0;
         bool alive = true;
@@ -339,7 +341,7 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             for (int i = 0; i < n; ++i, ++g) {
                 const int blk = 2 * (u.t0 + i) + (int)rank;
                 const int32_t row = pw.row(blk);
-                if ((g & 1u) != mine) continue;
+                if (kFp8 && (g & 1u) != mine) continue;
                 int ok = 1;
                 const int s = (int)(g & 1u);
                 const uint32_t slot = sbase + kOffK + s * kKSlotBytes;
@@ -391,34 +393,97 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             }
         }
         drain_on_abort();
+    } else if (!kFp8 && warp == 3) {
+        // ------------------------------------------------------------ partner V (bf16 cache)
+        // Two 16 KB loads of the partner's page once the tile's S MMAs are done.  A tile whose pages
+        // reach past L: the rows there are cleared, in this CTA's own V chunks and in the partner's
+        // once they landed, before the leader is told.
+        uint32_t g = 0, ntail = 0;
+        bool alive = true;
+        Unit u;
+        while (alive && iter.next(p, u)) {
+            const int n = u.tiles();
+            if (n <= 0) continue;
+            PageWindow pw;
+            pw.init(p.block_table + (int64_t)u.b * p.bt_stride, 2 * u.t0, u.kb1, lane, p.num_pages, false);
+            for (int i = 0; i < n; ++i, ++g) {
+                const int blk = 2 * (u.t0 + i) + 1 - (int)rank;
+                const int32_t row = pw.row(blk);
+                const int s = (int)(g & 1u);
+                const uint32_t slot = sbase + kOffK + s * kKSlotBytes;
+                const int own_valid = u.L - (blk ^ 1) * kPage, valid = u.L - blk * kPage;
+                const bool cut = (own_valid < kPage && (blk ^ 1) < u.kb1) || (valid < kPage && blk < u.kb1);
+                int ok = 1;
+                if (lane == 0) {
+                    ok = mbar_wait_bounded(bar(kBarQKDone + s), (g >> 1) & 1u, actl);
+                    if (ok) {
+                        if (cut) mbar_arrive_expect_tx(bar(kBarVTail), 2 * 2 * kBox);
+#pragma unroll
+                        for (int nn = 0; nn < 2; ++nn) {
+                            const uint32_t vf = bar(kBarVFull + 2 * s + nn);
+                            if (!cut && leader) mbar_arrive_expect_tx(vf, 2 * 2 * kBox);
+                            const uint32_t dst = slot + (4 * nn + 2 * (1 - (int)rank)) * kBox;
+                            if (cut)
+                                tma_load_3d(dst, &v_map, bar(kBarVTail), 0, row, 4 * nn + 2 * (int)rank);
+                            else
+                                tma_load_3d_pair(dst, &v_map, map_to_cta(vf, 0), 0, row, 4 * nn + 2 * (int)rank);
+                        }
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (ok && cut) {
+                    if (own_valid < kPage) clear_v_rows(slot, 2 * (int)rank, own_valid, lane);
+                    const bool landed = mbar_wait_bounded(bar(kBarVTail), ntail & 1u, actl);
+                    ok = __all_sync(0xffffffffu, landed);
+                    if (valid < kPage) clear_v_rows(slot, 2 * (1 - (int)rank), valid, lane);
+                    fence_proxy_async_smem();
+                    signal_leader(kBarVFull + 2 * s, 8);
+                    signal_leader(kBarVFull + 2 * s + 1, 9);
+                    ++ntail;
+                }
+                if (!ok) {
+                    alive = false;
+                    break;
+                }
+            }
+        }
+        drain_on_abort();
     } else if (warp >= kQWarp0 && warp < kQWarp0 + 4) {
-        // ------------------------------------------------------------ Q and partner V
+        // ------------------------------------------------------------ Q (8-bit cache: and partner V)
         const int quarter = warp & 3;
         const int qt = threadIdx.x - kQWarp0 * 32;          // 0..127
         const int rloc = (32 * quarter + lane) & 63;
         const int rtile = kCtaRows * (int)rank + rloc;      // row of the unit's tile
         const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
-        uint32_t uq = 0, g = 0, ntail = 0;
+        uint32_t uq = 0, g = 0;
         bool q_range = false, alive = true;
         Unit u;
         while (alive && iter.next(p, u)) {
             const int n = u.tiles();
             if (n <= 0) continue;
-            // ---- Q of the unit (rows past its last read as zeros)
-            if (uq > 0 && !mbar_wait_bounded(bar(kBarQEmpty), (uq - 1) & 1u, actl)) break;
+            // ---- Q of the unit (rows past its last repeat it: computed, never stored): columns
+            // [256, 576) into shared memory, columns [0, 256) into tensor memory, each row twice
+            // (lane r and 64 + r).  The first half's loads go out before the unit before is done
+            // with Q.
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)u.row0 + min(rtile, u.nrows - 1)) * kDqk);
+            uint4 v[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = __ldg(src + k);
+            const bool free = uq == 0 || mbar_wait_bounded(bar(kBarQEmpty), (uq - 1) & 1u, actl);
+            if (!__all_sync(0xffffffffu, free)) break;
             tc_fence_after();
             if (!kFp8 && quarter == 3 && lane == 0) {
                 if (leader) mbar_arrive_expect_tx(bar(kBarQFull), 2 * kQHiBytes);
                 tma_load_3d_pair(sbase + kOffQ, &q_map, map_to_cta(bar(kBarQFull), 0), 0,
                                  u.row0 + kCtaRows * (int)rank, kQLoChunks);
             }
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)u.row0 + rtile) * kDqk);
-            const bool have = rtile < u.nrows;
+            __syncwarp();
 #pragma unroll
             for (int hb = 0; hb < 2; ++hb) {
-                uint4 v[16];   // 128 of the row's columns [0, 256): their loads in flight at once
+                if (hb == 1) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = have ? __ldg(src + 16 * hb + k) : make_uint4(0, 0, 0, 0);
+                    for (int k = 0; k < 16; ++k) v[k] = __ldg(src + 16 + k);
+                }
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t w[16];
@@ -437,87 +502,47 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 }
             }
             if constexpr (kFp8) {
-                // Q columns [256, 576) as f16 into shared memory (128-byte swizzle): lane
-                // quarters 0 / 1 take chunks 0..2 of them, quarters 2 / 3 chunks 3..4
+                // Q columns [256, 576) as f16 (128-byte swizzle): lane quarters 0 / 1 take chunks
+                // 0..2 of them, quarters 2 / 3 chunks 3..4
                 const int c0 = quarter < 2 ? 0 : 3, c1 = quarter < 2 ? 3 : kQHiChunks;
 #pragma unroll 1
                 for (int cc = c0; cc < c1; ++cc) {
                     const uint32_t qrow = sbase + kOffQ + cc * kBox + (uint32_t)rloc * 128u;
-                    uint4 v[8];
+                    uint4 x[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = have ? __ldg(src + 32 + 8 * cc + k) : make_uint4(0, 0, 0, 0);
+                    for (int k = 0; k < 8; ++k) x[k] = __ldg(src + 32 + 8 * cc + k);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         st_shared_v4u(qrow + 16u * ((uint32_t)k ^ ((uint32_t)rloc & 7u)),
-                                      decode::bf16x2_to_f16x2(v[k].x, q_range), decode::bf16x2_to_f16x2(v[k].y, q_range),
-                                      decode::bf16x2_to_f16x2(v[k].z, q_range), decode::bf16x2_to_f16x2(v[k].w, q_range));
+                                      decode::bf16x2_to_f16x2(x[k].x, q_range), decode::bf16x2_to_f16x2(x[k].y, q_range),
+                                      decode::bf16x2_to_f16x2(x[k].z, q_range), decode::bf16x2_to_f16x2(x[k].w, q_range));
                 }
                 fence_proxy_async_smem();
                 if (__any_sync(0xffffffffu, q_range) && lane == 0) raise_error(32 /* MLA_DEVERR_Q_RANGE */);
+                __syncwarp();
             }
             tc_wait_st();
             tc_fence_before();
             signal_leader(kBarQFull, 14 + quarter);
             ++uq;
-            // ---- partner V of each tile of the unit
-            const int32_t* bt_row = p.block_table + (int64_t)u.b * p.bt_stride;
-            for (int i = 0; i < n; ++i, ++g) {
-                const int blk = 2 * (u.t0 + i) + 1 - (int)rank;
-                int pg = blk < u.kb1 ? __ldg(bt_row + blk) : -1;
-                if (pg < 0 || (int64_t)pg >= p.num_pages) pg = -1;   // reported by the K loads
-                const int s = (int)(g & 1u);
-                const uint32_t slot = sbase + kOffK + s * kKSlotBytes;
-                if constexpr (!kFp8) {
-                    if (quarter == 3) {
-                        // two 16 KB loads once the tile's S MMAs are done.  A tile whose pages reach
-                        // past L: the rows there are cleared, in this CTA's own V chunks and in the
-                        // partner's once they landed, before the leader is told.
-                        const int own_valid = u.L - (blk ^ 1) * kPage, valid = u.L - blk * kPage;
-                        const bool cut = (own_valid < kPage && (blk ^ 1) < u.kb1) || (valid < kPage && blk < u.kb1);
-                        int ok = 1;
-                        if (lane == 0) {
-                            ok = mbar_wait_bounded(bar(kBarQKDone + s), (g >> 1) & 1u, actl);
-                            if (ok) {
-                                const int32_t row = pg >= 0 ? pg * kPage : (int32_t)(p.num_pages * kPage);
-                                if (cut) mbar_arrive_expect_tx(bar(kBarVTail), 2 * 2 * kBox);
-#pragma unroll
-                                for (int nn = 0; nn < 2; ++nn) {
-                                    const uint32_t vf = bar(kBarVFull + 2 * s + nn);
-                                    if (!cut && leader) mbar_arrive_expect_tx(vf, 2 * 2 * kBox);
-                                    const uint32_t dst = slot + (4 * nn + 2 * (1 - (int)rank)) * kBox;
-                                    if (cut)
-                                        tma_load_3d(dst, &v_map, bar(kBarVTail), 0, row, 4 * nn + 2 * (int)rank);
-                                    else
-                                        tma_load_3d_pair(dst, &v_map, map_to_cta(vf, 0), 0, row, 4 * nn + 2 * (int)rank);
-                                }
-                            }
-                        }
-                        ok = __shfl_sync(0xffffffffu, ok, 0);
-                        if (ok && cut) {
-                            if (own_valid < kPage) clear_v_rows(slot, 2 * (int)rank, own_valid, lane);
-                            const bool landed = mbar_wait_bounded(bar(kBarVTail), ntail & 1u, actl);
-                            ok = __all_sync(0xffffffffu, landed);
-                            if (valid < kPage) clear_v_rows(slot, 2 * (1 - (int)rank), valid, lane);
-                            fence_proxy_async_smem();
-                            signal_leader(kBarVFull + 2 * s, 8);
-                            signal_leader(kBarVFull + 2 * s + 1, 9);
-                            ++ntail;
-                        }
-                        if (!ok) {
-                            alive = false;
-                            break;
-                        }
-                    }
-                } else {
-                    // 4 chunks x 64 rows x 4 sixteen-byte units of 8-bit values: 8 per thread,
-                    // widened to f16 on the way into the slot, rows at or past L as zeros
+            if constexpr (kFp8) {
+                // ---- partner V of each tile: 4 chunks x 64 rows x 4 sixteen-byte units of 8-bit
+                // values, 8 per thread, widened to f16 on the way into the slot once the tile's S
+                // MMAs are done, rows at or past L as zeros
+                const int32_t* bt_row = p.block_table + (int64_t)u.b * p.bt_stride;
+                for (int i = 0; i < n; ++i, ++g) {
+                    const int blk = 2 * (u.t0 + i) + 1 - (int)rank;
+                    int pg = blk < u.kb1 ? __ldg(bt_row + blk) : -1;
+                    if (pg < 0 || (int64_t)pg >= p.num_pages) pg = -1;   // reported by the K loads
+                    const int s = (int)(g & 1u);
+                    const uint32_t slot = sbase + kOffK + s * kKSlotBytes;
                     const int valid = u.L - blk * kPage;
-                    uint4 v[8];
+                    uint4 w[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int x = qt + 128 * j, hh = x >> 8, row = (x >> 2) & 63, q4 = x & 3;
                         const int chunk = 4 * (hh >> 1) + 2 * (int)rank + (hh & 1);
-                        v[j] = pg >= 0 && row < valid ? __ldg(reinterpret_cast<const uint4*>(
+                        w[j] = pg >= 0 && row < valid ? __ldg(reinterpret_cast<const uint4*>(
                                              p.kv + ((int64_t)pg * kPage + row) * kDqk + chunk * 64 + q4 * 16))
                                        : make_uint4(0, 0, 0, 0);
                     }
@@ -532,12 +557,12 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                         const int pos = 4 * (hh >> 1) + 2 * (1 - (int)rank) + (hh & 1);
                         const uint32_t r = slot + pos * kBox + row * 128;
                         const uint32_t sw = (uint32_t)row & 7u;
-                        st_shared_v4u(r + 16u * ((2u * q4) ^ sw), fp8x2_to_f16x2<kE5M2>(v[j].x),
-                                      fp8x2_to_f16x2<kE5M2>(v[j].x >> 16), fp8x2_to_f16x2<kE5M2>(v[j].y),
-                                      fp8x2_to_f16x2<kE5M2>(v[j].y >> 16));
-                        st_shared_v4u(r + 16u * ((2u * q4 + 1u) ^ sw), fp8x2_to_f16x2<kE5M2>(v[j].z),
-                                      fp8x2_to_f16x2<kE5M2>(v[j].z >> 16), fp8x2_to_f16x2<kE5M2>(v[j].w),
-                                      fp8x2_to_f16x2<kE5M2>(v[j].w >> 16));
+                        st_shared_v4u(r + 16u * ((2u * q4) ^ sw), fp8x2_to_f16x2<kE5M2>(w[j].x),
+                                      fp8x2_to_f16x2<kE5M2>(w[j].x >> 16), fp8x2_to_f16x2<kE5M2>(w[j].y),
+                                      fp8x2_to_f16x2<kE5M2>(w[j].y >> 16));
+                        st_shared_v4u(r + 16u * ((2u * q4 + 1u) ^ sw), fp8x2_to_f16x2<kE5M2>(w[j].z),
+                                      fp8x2_to_f16x2<kE5M2>(w[j].z >> 16), fp8x2_to_f16x2<kE5M2>(w[j].w),
+                                      fp8x2_to_f16x2<kE5M2>(w[j].w >> 16));
                         if (j == 3 || j == 7) {   // an output block's two chunks are in place
                             fence_proxy_async_smem();
                             signal_leader(kBarVFull + 2 * s + (j >> 2), 8 + quarter);
@@ -546,7 +571,7 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 }
             }
         }
-        if (!kFp8 && quarter == 3) drain_on_abort();
+        drain_on_abort();
     } else if (warp == 1) {
         // ------------------------------------------------------------ S issuer (leader)
         // A warp each for S and PV, so that neither waits behind the other's barriers; the whole
