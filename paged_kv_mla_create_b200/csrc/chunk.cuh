@@ -66,10 +66,11 @@ constexpr int kHiBoxes = kChunks - kLoBoxes;
 constexpr int kOffQ = 0;                            // Q chunks 4..8
 constexpr int kOffK = kOffQ + kQHiBytes;
 constexpr int kOffP = kOffK + kKSlots * kKSlotBytes;
-constexpr int kOffX = kOffP + kPBytes;              // row-max exchange: 2 x 256 floats, row sums 256
-constexpr int kOffStage = kOffX + 3072;             // epilogue staging of warps 12..15: 32 rows x 128 B each
-constexpr int kOffPSig = kOffStage + 4 * 32 * 128;  // leader: landing words of the peer's signals
-constexpr int kOffBar = kOffPSig + 256;             // words: P 0..7, V 8..11, K 12, 13, Q 14..17, S 18..25, O 26..33
+constexpr int kOffX = kOffP + kPBytes;              // row-max exchange 2 x 256 floats; of two finished
+                                                    // units each: row sums 256, row maxima 64
+constexpr int kUnitSums = 2 * kSoftmaxThreads, kUnitSumsStride = kSoftmaxThreads + kCtaRows;   // floats
+constexpr int kOffPSig = kOffX + 5120;              // leader: landing words of the peer's signals
+constexpr int kOffBar = kOffPSig + 256;             // words: P 0..7, V 8..11, K 12, 13, Q 14..17, S 18..25, O 26..29
 
 enum : int {
     kBarKFull = 0,                      // leader (slot, half): both CTAs' chunks 0..3 / 4..8 landed
@@ -83,17 +84,17 @@ enum : int {
     kBarPFull = kBarSFree + 2,          // leader: 16 softmax warps wrote P
     kBarPvDone,                         // both: the PV MMAs of a tile finished (P reusable)
     kBarOFull,                          // both: the unit's last PV finished
-    kBarOEmpty,                         // leader: 16 softmax warps read O out
+    kBarOEmpty,                         // leader: 8 Q warps read O out
     kBarXchg,                           // local (x2): the 8 softmax warps posted row maxima
-    kBarLx = kBarXchg + 2,              // local: the 8 softmax warps posted row sums
-    kBarVTail,                          // local: the partner V of a tile with a cut page landed
+    kBarLx = kBarXchg + 2,              // local (x2): the 8 softmax warps posted a unit's row sums and maxima
+    kBarVTail = kBarLx + 2,             // local: the partner V of a tile with a cut page landed
     kBarKRaw,                           // local (x2), 8-bit cache: this CTA's page landed
     kNumBars = kBarKRaw + kKSlots
 };
 constexpr int kOffMisc = kOffBar + kNumBars * 8;    // tensor-memory base, abort flag
 constexpr int kSmemBytes = kOffMisc + 64 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-static_assert(kOffK % 1024 == 0 && kOffP % 1024 == 0 && kOffStage % 1024 == 0,
+static_assert(kOffK % 1024 == 0 && kOffP % 1024 == 0,
               "128-byte swizzle atoms need 1 KB alignment");
 static_assert(kOffBar % 8 == 0, "mbarriers are 8 bytes");
 
@@ -105,7 +106,7 @@ struct Params {
     const uint8_t* kv;             // [num_pages * 64, 576]
     const int32_t* block_table;    // [bs, bt_stride]
     int64_t bt_stride;
-    int32_t max_pages;
+    int32_t max_keys;              // positions the table has columns for (64 per column)
     const int32_t* cache_seqlens;  // [bs]
     const int32_t* cu;             // [bs + 1]
     const int32_t* plan;           // [parts, 8]
@@ -126,7 +127,7 @@ struct Params {
 // A unit, or the piece of it that lies in this part: request b, query rows row0 + [0, nrows) of q,
 // key tiles [t0, t1), pages [2 t0, kb1); slot: where the piece's partial goes (-1: the whole unit).
 struct Unit {
-    int b, tok0, row_in_req, nrows, n, L, t0, t1, kb1, slot;
+    int b, row_in_req, nrows, n, L, t0, t1, kb1, slot;
     int row0;   // first row in q / out
     __device__ int tiles() const { return t1 - t0; }
 };
@@ -144,24 +145,25 @@ __device__ __forceinline__ void request_rows(const int32_t* cu, int b, int num_t
 struct UnitIter {
     int b, m, t, b1, m1, t1;
     int part;
+    int cb, c0, n, L;   // rows and length of request cb, kept while its units follow one another
     __device__ bool next(const Params& p, Unit& u) {
         while (b < p.bs && (b < b1 || (b == b1 && (m < m1 || (m == m1 && t < t1))))) {
-            int c0, n;
-            request_rows(p.cu, b, p.num_tokens, c0, n);
+            if (cb != b) {
+                request_rows(p.cu, b, p.num_tokens, c0, n);
+                L = p.cache_seqlens[b];
+                cb = b;
+            }
             const int rows = n * p.h;
             if (m >= (rows + kTileRows - 1) / kTileRows) {
                 ++b;
                 m = t = 0;
                 continue;
             }
-            const int L = p.cache_seqlens[b];
-            int64_t keys = unit_keys(L, n, p.h, m, p.causal);
-            if (keys > (int64_t)p.max_pages * kPage) keys = (int64_t)p.max_pages * kPage;
-            const int tiles = (int)((keys + kTileKeys - 1) / kTileKeys);
+            const int keys = min(unit_keys(L, n, p.h, m, p.causal), p.max_keys);
+            const int tiles = (keys + kTileKeys - 1) / kTileKeys;
             const int hi = (b == b1 && m == m1) ? min(t1, tiles) : tiles;
             const int lo = t;
             u.b = b;
-            u.tok0 = c0;
             u.n = n;
             u.L = L;
             u.row_in_req = m * kTileRows;
@@ -169,13 +171,19 @@ struct UnitIter {
             u.row0 = c0 * p.h + m * kTileRows;
             u.t0 = lo;
             u.t1 = hi;
-            u.kb1 = min(2 * hi, (int)((keys + kPage - 1) / kPage));
+            u.kb1 = min(2 * hi, (keys + kPage - 1) / kPage);
             u.slot = lo > 0 ? 2 * part : (hi < tiles ? 2 * part + 1 : -1);
             ++m;
             t = 0;
             if (lo >= hi && lo > 0) continue;   // nothing left of a unit whose keys end before the cut
             return true;
         }
+        return false;
+    }
+    // The next unit that has keys (the roles that only feed the MMAs skip the others).
+    __device__ bool next_tiles(const Params& p, Unit& u) {
+        while (next(p, u))
+            if (u.tiles() > 0) return true;
         return false;
     }
 };
@@ -191,6 +199,8 @@ __device__ __forceinline__ UnitIter make_iter(const Params& p, int part, bool& o
     it.m1 = r1.x;
     it.t1 = r1.y;
     it.part = part;
+    it.cb = -1;
+    it.c0 = it.n = it.L = 0;
     ok = it.b >= 0 && it.b <= it.b1 && it.b1 <= p.bs && it.m >= 0 && it.t >= 0 && it.m1 >= 0 && it.t1 >= 0;
     if (!ok) it.b = p.bs;   // no units
     return it;
@@ -233,8 +243,8 @@ __device__ __forceinline__ void clear_v_rows(uint32_t slot, int c, int valid, in
 template <int kKv>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap klo_map,
-                 const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap o_map,
-                 const __grid_constant__ CUtensorMap ps_map, const __grid_constant__ Params p) {
+                 const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map,
+                 const __grid_constant__ Params p) {
     constexpr bool kFp8 = kKv != 0;
     constexpr bool kE5M2 = kKv == 2;
     extern __shared__ uint8_t smem_raw[];
@@ -268,12 +278,12 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             mbar_init(bar(kBarSFull + j), 1);
             mbar_init(bar(kBarSFree + j), kSoftmaxWarps);
             mbar_init(bar(kBarXchg + j), kSoftmaxWarps);
+            mbar_init(bar(kBarLx + j), kSoftmaxWarps);
         }
         mbar_init(bar(kBarPFull), kSoftmaxWarps);
         mbar_init(bar(kBarPvDone), 1);
         mbar_init(bar(kBarOFull), 1);
-        mbar_init(bar(kBarOEmpty), kSoftmaxWarps);
-        mbar_init(bar(kBarLx), kSoftmaxWarps);
+        mbar_init(bar(kBarOEmpty), 4);
         mbar_init(bar(kBarVTail), 1);
         *abort_flag = 0;
         fence_mbarrier_init_cluster();
@@ -287,8 +297,6 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
         prefetch_tensormap(&klo_map);
         prefetch_tensormap(&v_map);
         prefetch_tensormap(&q_map);
-        prefetch_tensormap(&o_map);
-        prefetch_tensormap(&ps_map);
     }
     tc_fence_before();
     __syncthreads();
@@ -302,7 +310,6 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
     UnitIter iter = make_iter(p, part, plan_ok);
     const uint32_t tmem = *tmem_slot;
     const AbortCtl actl{abort_flag, map_to_cta(smem_u32(tmem_slot + 1), rank ^ 1u), p.wait_budget_ns};
-    const uint64_t part_pol = l2_policy_evict_last();
     if (!plan_ok && threadIdx.x == 0) raise_error(8 /* MLA_DEVERR_BAD_METADATA */);
 
     // A warp reporting to the leader's MMA issuer: the leader's warp arrives with expect_tx of 4
@@ -333,9 +340,8 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
         uint32_t g = 0;
         bool alive = true;
         Unit u;
-        while (alive && iter.next(p, u)) {
+        while (alive && iter.next_tiles(p, u)) {
             const int n = u.tiles();
-            if (n <= 0) continue;
             PageWindow pw;
             pw.init(p.block_table + (int64_t)u.b * p.bt_stride, 2 * u.t0, u.kb1, lane, p.num_pages, warp == 0);
             for (int i = 0; i < n; ++i, ++g) {
@@ -401,9 +407,8 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
         uint32_t g = 0, ntail = 0;
         bool alive = true;
         Unit u;
-        while (alive && iter.next(p, u)) {
+        while (alive && iter.next_tiles(p, u)) {
             const int n = u.tiles();
-            if (n <= 0) continue;
             PageWindow pw;
             pw.init(p.block_table + (int64_t)u.b * p.bt_stride, 2 * u.t0, u.kb1, lane, p.num_pages, false);
             for (int i = 0; i < n; ++i, ++g) {
@@ -449,18 +454,76 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
         }
         drain_on_abort();
     } else if (warp >= kQWarp0 && warp < kQWarp0 + 4) {
-        // ------------------------------------------------------------ Q (8-bit cache: and partner V)
+        // ------------------------------------------------------------ Q, o (8-bit cache: and partner V)
+        // These warps bring a unit's Q, then write the result of the unit before while the softmax
+        // warps are at the new unit's first tile already.
         const int quarter = warp & 3;
         const int qt = threadIdx.x - kQWarp0 * 32;          // 0..127
         const int rloc = (32 * quarter + lane) & 63;
         const int rtile = kCtaRows * (int)rank + rloc;      // row of the unit's tile
         const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
-        uint32_t uq = 0, g = 0;
+        const int half = quarter >> 1;                      // lanes of O's columns [0, 128) / [128, 256) of a block
+        const float dk = p.descale_k ? *p.descale_k : 1.0f;
+        const float* xmax = reinterpret_cast<const float*>(smem + kOffX);
+        uint32_t uq = 0, g = 0, ue = 0;
         bool q_range = false, alive = true;
-        Unit u;
-        while (alive && iter.next(p, u)) {
+        Unit u, done;
+        // o (or the piece's fp32 partial, normalised) and lse of unit `done`: 32 tensor-memory columns
+        // at a time, each thread writing whole 32-byte sectors of its row (64 bytes of bf16, 128 of
+        // fp32): nothing is staged, no store is waited for.
+        auto epilogue = [&]() -> bool {
+            const bool full = mbar_wait_bounded(bar(kBarOFull), ue & 1u, actl);
+            const bool sums = mbar_wait_bounded(bar(kBarLx + (ue & 1u)), (ue >> 1) & 1u, actl);
+            if (!__all_sync(0xffffffffu, full && sums)) return false;
+            tc_fence_after();
+            const float* x = xmax + kUnitSums + (ue & 1u) * kUnitSumsStride + rloc;
+            const float l_run = (x[0] + x[64]) + (x[128] + x[192]);
+            const float m_run = x[kSoftmaxThreads];
+            const float inv = l_run > 0.f ? dk / l_run : 0.f;
+            const float lse_val = l_run > 0.f ? (m_run + __log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+            const bool direct = done.slot < 0, write = !direct || rtile < done.nrows;
+            __nv_bfloat16* const orow = p.out + ((int64_t)done.row0 + rtile) * kDv + 128 * half;
+            float* const prow = p.part_o + ((int64_t)done.slot * kTileRows + rtile) * kDv + 128 * half;
+#pragma unroll 1
+            for (int st = 0; st < 8; ++st) {
+                uint32_t raw[32];
+                const uint32_t src = tmem + lane_off + kTmemO + 32u * st;
+                tmem_ld16(src, *reinterpret_cast<uint32_t(*)[16]>(raw));
+                tmem_ld16(src + 16u, *reinterpret_cast<uint32_t(*)[16]>(raw + 16));
+                tc_wait_ld();
+                if (st == 7) {
+                    tc_fence_before();
+                    signal_leader(kBarOEmpty, 26 + quarter);   // O is free for the next unit
+                }
+                const int col = 256 * (st >> 2) + 32 * (st & 3);
+                if (write) {
+                    if (direct) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            w[k] = pack_bf16x2(__uint_as_float(raw[2 * k]) * inv, __uint_as_float(raw[2 * k + 1]) * inv);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) st_global_v8(orow + col + 16 * k, w + 8 * k);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) raw[k] = __float_as_uint(__uint_as_float(raw[k]) * inv);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) st_global_v8(prow + col + 8 * k, raw + 8 * k);
+                    }
+                }
+                __syncwarp();
+            }
+            if (half == 0) {
+                if (!direct)
+                    p.part_lse[(int64_t)done.slot * kTileRows + rtile] = lse_val;
+                else if (rtile < done.nrows)
+                    p.lse[(int64_t)done.row0 + rtile] = lse_val;
+            }
+            ++ue;
+            return true;
+        };
+        while (alive && iter.next_tiles(p, u)) {
             const int n = u.tiles();
-            if (n <= 0) continue;
             // ---- Q of the unit (rows past its last repeat it: computed, never stored): columns
             // [256, 576) into shared memory, columns [0, 256) into tensor memory, each row twice
             // (lane r and 64 + r).  The first half's loads go out before the unit before is done
@@ -524,6 +587,17 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             tc_wait_st();
             tc_fence_before();
             signal_leader(kBarQFull, 14 + quarter);
+            {
+                // the unit after this one: its query rows into L2
+                UnitIter peek = iter;
+                Unit nu;
+                if (peek.next_tiles(p, nu) && rtile < nu.nrows) {
+                    const uint8_t* row = reinterpret_cast<const uint8_t*>(p.q + ((int64_t)nu.row0 + rtile) * kDqk);
+                    for (int k = half; k < 9; k += 2) prefetch_l2(row + 128 * k);
+                }
+            }
+            if (uq > 0 && !epilogue()) break;
+            done = u;
             ++uq;
             if constexpr (kFp8) {
                 // ---- partner V of each tile: 4 chunks x 64 rows x 4 sixteen-byte units of 8-bit
@@ -546,8 +620,8 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                                              p.kv + ((int64_t)pg * kPage + row) * kDqk + chunk * 64 + q4 * 16))
                                        : make_uint4(0, 0, 0, 0);
                     }
-                    const bool done = mbar_wait_bounded(bar(kBarQKDone + s), (g >> 1) & 1u, actl);
-                    if (!__all_sync(0xffffffffu, done)) {
+                    const bool s_done = mbar_wait_bounded(bar(kBarQKDone + s), (g >> 1) & 1u, actl);
+                    if (!__all_sync(0xffffffffu, s_done)) {
                         alive = false;
                         break;
                     }
@@ -571,6 +645,7 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 }
             }
         }
+        if (alive && ue < uq) epilogue();
         drain_on_abort();
     } else if (warp == 1) {
         // ------------------------------------------------------------ S issuer (leader)
@@ -583,9 +658,8 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 return __all_sync(0xffffffffu, mbar_wait_bounded(bar(b), parity, actl));
             };
             Unit u;
-            while (alive && iter.next(p, u)) {
+            while (alive && iter.next_tiles(p, u)) {
                 const int n = u.tiles();
-                if (n <= 0) continue;
                 if (!wait(kBarQFull, uq & 1u)) break;
                 for (int i = 0; i < n; ++i, ++g) {
                     const int s = (int)(g & 1u);
@@ -631,9 +705,8 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 return __all_sync(0xffffffffu, mbar_wait_bounded(bar(b), parity, actl));
             };
             Unit u;
-            while (alive && iter.next(p, u)) {
+            while (alive && iter.next_tiles(p, u)) {
                 const int n = u.tiles();
-                if (n <= 0) continue;
                 if (uq > 0 && !wait(kBarOEmpty, (uq - 1) & 1u)) break;
                 for (int i = 0; i < n; ++i, ++g) {
                     const int s = (int)(g & 1u);
@@ -677,10 +750,8 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
         const int sw8 = quarter + 4 * sub;                    // softmax warp 0..7
         const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
         const int rtile = kCtaRows * (int)rank + rloc;        // row of the unit's tile
-        const float dq = p.descale_q ? *p.descale_q : 1.0f;
-        const float dk = p.descale_k ? *p.descale_k : 1.0f;
-        const float sl2 = p.scale_log2 * dq * dk;
-        float* xmax = reinterpret_cast<float*>(smem + kOffX);  // [2][256] row maxima, [256] sums
+        const float sl2 = p.scale_log2 * (p.descale_q ? *p.descale_q : 1.0f) * (p.descale_k ? *p.descale_k : 1.0f);
+        float* xmax = reinterpret_cast<float*>(smem + kOffX);  // the exchange area
         const uint32_t swz = (uint32_t)(rloc & 7);
         auto post = [&](int b) {   // this warp's shared-memory posts are done
             __syncwarp();
@@ -704,7 +775,7 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             }
             int lim = u.L;
             if (p.causal) {
-                const int64_t l = (int64_t)u.L - u.n + (u.row_in_req + rtile) / p.h + 1;
+                const int64_t l = (int64_t)u.L - u.n + (int)((unsigned)(u.row_in_req + rtile) / (unsigned)p.h) + 1;
                 lim = l < u.L ? (int)l : u.L;
             }
             if (lim > u.kb1 * kPage) lim = u.kb1 * kPage;   // keys of this piece (and of the table) only
@@ -819,96 +890,17 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 signal_leader(kBarPFull, sw8);
             }
             if (!alive) break;
-            // ---- epilogue of the unit: o (or the piece's fp32 partial, normalised) and lse
-            if (!mbar_wait_bounded(bar(kBarOFull), uq & 1u, actl)) break;
-            tc_fence_after();
-            xmax[2 * kSoftmaxThreads + 128 * sub + t] = l_part;
-            post(kBarLx);
-            if (!mbar_wait_bounded(bar(kBarLx), uq & 1u, actl)) break;
-            float l_run;
+            // The unit's row sums and maxima, for the warps that write its result: two places and two
+            // barriers in turn, since a unit of one tile can end here before the unit before has been
+            // written (the one before that has: this unit's P waited for the PV that followed it).
             {
-                const float* x = xmax + 2 * kSoftmaxThreads + rloc;
-                l_run = (x[0] + x[64]) + (x[128] + x[192]);
-            }
-            const float inv = l_run > 0.f ? dk / l_run : 0.f;
-            const float lse_val = l_run > 0.f ? (m_run + __log2f(l_run)) * 0.69314718055994531f : -INFINITY;
-            const bool direct = u.slot < 0;
-            {
-                // Each warp has 32 rows x 128 tensor-memory columns (output block `sub`), 64 a step,
-                // staged 32 rows x 128 bytes at a time (128-byte swizzle) in 4 KB of its own: of the
-                // P buffer (idle: the next P is written after the next tile's row-max exchange, in
-                // which every softmax warp takes part) or of the staging area.
-                const uint32_t stage = sbase + (sub ? kOffStage : kOffP) + (uint32_t)quarter * 4096u;
-                uint32_t npass = 0;
-                const int r0 = kCtaRows * (int)rank + 32 * (quarter & 1);   // the warp's first row
-                const int rows = min(32, u.nrows - r0);   // of its rows in the unit (<= 0: none)
-#pragma unroll 1
-                for (int st = 0; st < 2; ++st) {
-                    uint32_t raw[64];
-                    const uint32_t src = tmem + lane_off + kTmemO + 128u * sub + 64u * st;
-                    tmem_ld16(src, *reinterpret_cast<uint32_t(*)[16]>(raw));
-                    tmem_ld16(src + 16u, *reinterpret_cast<uint32_t(*)[16]>(raw + 16));
-                    tmem_ld16(src + 32u, *reinterpret_cast<uint32_t(*)[16]>(raw + 32));
-                    tmem_ld16(src + 48u, *reinterpret_cast<uint32_t(*)[16]>(raw + 48));
-                    tc_wait_ld();
-                    if (st == 1) {
-                        tc_fence_before();
-                        signal_leader(kBarOEmpty, 26 + sw8);   // O is free for the next unit
-                    }
-#pragma unroll
-                    for (int pass = 0; pass < 2; ++pass) {
-                        if (direct && pass == 1) break;
-                        uint32_t w[32];
-                        int col = 256 * sub + 128 * half + 64 * st;
-                        if (direct) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                w[k] = pack_bf16x2(__uint_as_float(raw[2 * k]) * inv, __uint_as_float(raw[2 * k + 1]) * inv);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(__uint_as_float(raw[32 * pass + k]) * inv);
-                            col += 32 * pass;
-                        }
-                        if (lane == 0 && npass >= 1) bulk_wait_read<0>();
-                        __syncwarp();
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            st_shared_v4u(stage + (uint32_t)lane * 128u + 16u * ((uint32_t)k ^ ((uint32_t)lane & 7u)),
-                                          w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (!direct || rows == 32) {
-                            // whole boxes go out as TMA stores (a partial's slot always has room for one)
-                            if (lane == 0) {
-                                if (direct)
-                                    tma_store_2d(&o_map, stage, col, u.row0 + r0);
-                                else
-                                    tma_store_2d_hint(&ps_map, stage, col, u.slot * kTileRows + r0, part_pol);
-                                bulk_commit();
-                            }
-                        } else {
-                            // the rows behind belong to another request or to nobody
-                            for (int r = lane >> 3; r < rows; r += 4) {
-                                const uint4 v = ld_shared_v4u(stage + (uint32_t)r * 128u + 16u * (((uint32_t)lane & 7u) ^ ((uint32_t)r & 7u)));
-                                *reinterpret_cast<uint4*>(p.out + ((int64_t)u.row0 + r0 + r) * kDv + col + 8 * (lane & 7)) = v;
-                            }
-                        }
-                        ++npass;
-                        __syncwarp();
-                    }
-                }
-            }
-            if (lane == 0) bulk_wait_read<0>();   // the staging (and the P buffer) free again
-            __syncwarp();
-            if (half == 0 && sub == 0) {
-                if (!direct)
-                    st_global_f32_hint(p.part_lse + (int64_t)u.slot * kTileRows + rtile, row_valid ? lse_val : -INFINITY, part_pol);
-                else if (row_valid)
-                    p.lse[(int64_t)u.row0 + rtile] = lse_val;
+                float* x = xmax + kUnitSums + (uq & 1u) * kUnitSumsStride;
+                x[128 * sub + t] = l_part;
+                if (sub == 0 && half == 0) x[kSoftmaxThreads + rloc] = m_run;
+                post(kBarLx + (uq & 1u));
             }
             ++uq;
         }
-        if (lane == 0) bulk_wait<0>();   // the epilogues' stores
     }
 
     tc_fence_before();
@@ -924,13 +916,75 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
 // exp(lse_i - lse) o_i, in part order.  Part i begins a cut unit when its end lies inside a unit
 // that it does not itself continue; its piece is slot 2 i + 1, and the parts after it that begin
 // inside the same unit hold the others in slot 2 j.  Every CTA lists the cut units from the plan
-// (before it waits for the attention grid: the plan is older than that grid), then the warps take
-// (unit, row, 128-column slice) in turn.  At most 2 x 256 KB of partials a part: latency bounds it.
+// (before it waits for the attention grid: the plan is older than that grid), then its warps take
+// whole rows in turn, 16 columns a lane, two pieces' loads in flight -- or, when the cut units'
+// rows are fewer than the warps (few units of many pieces), quarters of rows, 4 columns a lane and
+// eight pieces in flight.
 constexpr int kMergeThreads = 256;
+constexpr int kMergeCtasPerPart = 6;   // three CTAs an SM, all resident at once
 constexpr int kMergeMaxParts = 1024;
-constexpr int kMergeSlices = 4;   // 128 columns a warp, four a lane
 
-__global__ void __launch_bounds__(kMergeThreads)
+template <int kCols, int kAhead>
+__device__ __forceinline__ void merge_unit_row(const int32_t* __restrict__ plan, int2 tk, int row, int col0, int64_t orow,
+                                               const float* __restrict__ part_o, const float* __restrict__ part_lse,
+                                               __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int lane) {
+    const int pieces = tk.y + 1;
+    auto slot_row = [&](int k) { return (int64_t)(k == 0 ? 2 * tk.x + 1 : 2 * (tk.x + k)) * kTileRows + row; };
+    auto lse_of = [&](int k) -> float {
+        if (k >= pieces) return -INFINITY;
+        if (k > 0) {   // a part that begins inside the unit but holds none of it
+            const int32_t* e = plan + 8 * (int64_t)(tk.x + k);
+            if (e[0] == e[3] && e[1] == e[4] && e[2] >= e[5]) return -INFINITY;
+        }
+        return part_lse[slot_row(k)];
+    };
+    const float l0 = lse_of(lane);   // of the first 32 pieces, a lane each
+    float mx = l0;
+    for (int k = lane + 32; k < pieces; k += 32) mx = fmaxf(mx, lse_of(k));
+    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    float sum = 0.f;
+    if (mx != -INFINITY) {
+        sum = expf(l0 - mx);
+        for (int k = lane + 32; k < pieces; k += 32) sum += expf(lse_of(k) - mx);
+    }
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    const float total = mx != -INFINITY ? mx + logf(sum) : -INFINITY;
+    float acc[kCols];
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+    if (mx != -INFINITY) {
+        float wl = expf(l0 - total);
+        for (int k0 = 0; k0 < pieces; k0 += kAhead) {
+            if (k0 > 0 && (k0 & 31) == 0) wl = expf(lse_of(k0 + lane) - total);   // the next 32 pieces' weights
+            float4 v[kAhead][kCols / 4];
+            float wt[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                wt[j] = __shfl_sync(0xffffffffu, wl, (k0 + j) & 31);   // 0 past the last piece
+#pragma unroll
+                for (int c = 0; c < kCols / 4; ++c)
+                    v[j][c] = wt[j] > 0.f ? *reinterpret_cast<const float4*>(part_o + slot_row(k0 + j) * kDv + col0 + 128 * c + 4 * lane)
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+                for (int c = 0; c < kCols / 4; ++c) {
+                    acc[4 * c] += wt[j] * v[j][c].x;
+                    acc[4 * c + 1] += wt[j] * v[j][c].y;
+                    acc[4 * c + 2] += wt[j] * v[j][c].z;
+                    acc[4 * c + 3] += wt[j] * v[j][c].w;
+                }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < kCols / 4; ++c)
+        *reinterpret_cast<uint2*>(out + orow * kDv + col0 + 128 * c + 4 * lane) =
+            make_uint2(pack_bf16x2(acc[4 * c], acc[4 * c + 1]), pack_bf16x2(acc[4 * c + 2], acc[4 * c + 3]));
+    if (col0 == 0 && lane == 0) lse[orow] = total;
+}
+
+__global__ void __launch_bounds__(kMergeThreads, kMergeCtasPerPart / 2)
 chunk_merge_kernel(const int32_t* __restrict__ plan, const int32_t* __restrict__ cu, int32_t parts, int32_t bs, int32_t h,
                    int32_t num_tokens, const float* __restrict__ part_o, const float* __restrict__ part_lse,
                    __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
@@ -958,59 +1012,24 @@ chunk_merge_kernel(const int32_t* __restrict__ plan, const int32_t* __restrict__
     }
     __syncthreads();
     pdl_wait_prerequisites();
-    const int64_t total = (int64_t)ntask * kTileRows * kMergeSlices;
+    const int64_t warp = (int64_t)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
     const int64_t nwarps = (int64_t)gridDim.x * (kMergeThreads / 32);
-    for (int64_t w = (int64_t)blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5); w < total; w += nwarps) {
-        const int slice = (int)(w % kMergeSlices);
-        const int row = (int)(w / kMergeSlices % kTileRows);
-        const int2 tk = task[w / (kMergeSlices * kTileRows)];
+    const bool quarters = (int64_t)ntask * kTileRows < nwarps;
+    const int64_t total = (int64_t)ntask * kTileRows * (quarters ? 4 : 1);
+    for (int64_t w = warp; w < total; w += nwarps) {
+        const int64_t unit_row = quarters ? w >> 2 : w;
+        const int row = (int)(unit_row % kTileRows);
+        const int2 tk = task[unit_row / kTileRows];
         const int32_t* r = plan + 8 * (int64_t)tk.x;
         int c0, n;
         request_rows(cu, r[3], num_tokens, c0, n);
-        if ((int64_t)r[4] * kTileRows + row >= (int64_t)n * h) continue;
-        const int64_t orow = (int64_t)c0 * h + (int64_t)r[4] * kTileRows + row;
-        const int pieces = tk.y + 1;
-        auto slot_of = [&](int k) { return (int64_t)(k == 0 ? 2 * tk.x + 1 : 2 * (tk.x + k)); };
-        auto lse_of = [&](int k) -> float {
-            if (k > 0) {   // a part that begins inside the unit but holds none of it
-                const int32_t* e = plan + 8 * (int64_t)(tk.x + k);
-                if (e[0] == e[3] && e[1] == e[4] && e[2] >= e[5]) return -INFINITY;
-            }
-            return part_lse[slot_of(k) * kTileRows + row];
-        };
-        float mx = -INFINITY;
-        for (int k = lane; k < pieces; k += 32) mx = fmaxf(mx, lse_of(k));
-        for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        float sum = 0.f;
-        if (mx != -INFINITY)
-            for (int k = lane; k < pieces; k += 32) sum += expf(lse_of(k) - mx);
-        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const float total_lse = mx != -INFINITY ? mx + logf(sum) : -INFINITY;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int col = slice * 128 + 4 * lane;
-        if (mx != -INFINITY) {
-            for (int k0 = 0; k0 < pieces; k0 += 8) {
-                float4 v[8];
-                float wt[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int k = k0 + j;
-                    const float l = k < pieces ? lse_of(k) : -INFINITY;
-                    wt[j] = l != -INFINITY ? expf(l - total_lse) : 0.f;
-                    v[j] = l != -INFINITY ? *reinterpret_cast<const float4*>(part_o + (slot_of(k) * kTileRows + row) * kDv + col)
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    acc.x += wt[j] * v[j].x;
-                    acc.y += wt[j] * v[j].y;
-                    acc.z += wt[j] * v[j].z;
-                    acc.w += wt[j] * v[j].w;
-                }
-            }
-        }
-        *reinterpret_cast<uint2*>(out + orow * kDv + col) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-        if (slice == 0 && lane == 0) lse[orow] = total_lse;
+        const int64_t in_req = (int64_t)r[4] * kTileRows + row;
+        if (in_req >= (int64_t)n * h) continue;
+        const int64_t orow = (int64_t)c0 * h + in_req;
+        if (quarters)
+            merge_unit_row<4, 8>(plan, tk, row, 128 * (int)(w & 3), orow, part_o, part_lse, out, lse, lane);
+        else
+            merge_unit_row<16, 2>(plan, tk, row, 0, orow, part_o, part_lse, out, lse, lane);
     }
 }
 

@@ -52,12 +52,11 @@ struct MetaParams {
 // bounds the tile's keys.  Shared by the plan and the attention kernel, which must agree.
 __host__ __device__ __forceinline__ int unit_keys(int L, int n, int h, int m, int causal) {
     if (!causal) return L > 0 ? L : 0;
-    const int64_t rows = (int64_t)n * h;
-    int64_t last = (int64_t)m * kTileRows + kTileRows - 1;
-    if (last > rows - 1) last = rows - 1;
-    int64_t lim = (int64_t)L - n + last / h + 1;
-    if (lim > L) lim = L;
-    return lim > 0 ? (int)lim : 0;
+    // (n * h < 2^31: the callers' row counts are bounded so)
+    const unsigned rows = (unsigned)n * (unsigned)h, end = ((unsigned)m + 1u) * kTileRows;
+    const unsigned last = (end < rows ? end : rows) - 1u;
+    const int64_t lim = (int64_t)L - n + (int)(last / (unsigned)h) + 1;
+    return lim < L ? (lim > 0 ? (int)lim : 0) : (L > 0 ? L : 0);
 }
 
 // The plan's cost of the first m row tiles of a request: every tile costs kUnitCost plus its keys
@@ -77,6 +76,7 @@ struct MetaSmem {
     int32_t off[kMetaMaxRequests + 1];   // new pages before request b
     int32_t warp_n[kMetaThreads / 32], warp_p[kMetaThreads / 32];
     int64_t warp_c[kMetaThreads / 32];
+    int64_t cost[kMetaThreads];          // plan: cost before each thread's requests
 };
 
 __device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b, int32_t cap) {
@@ -187,8 +187,7 @@ __device__ __forceinline__ int32_t page_of(const MetaParams& a, const Req& r, in
 // The split plan: the units (query row tiles of 128 rows, in order) laid end to end by cost, cut
 // into `parts` ranges of equal cost; a range may begin or end inside a unit, at a key tile.  Row i
 // of the plan = [begin request, row tile, key tile, end request, row tile, key tile, 0, 0], the
-// end exclusive.  A thread places one cut: bisection over the requests' costs, then over the row
-// tiles by the closed form of units_cost, so the work does not grow with the tokens.
+// end exclusive.  A thread a cut; the work does not grow with the tokens.
 template <typename IdxT, typename LenT>
 __device__ __forceinline__ void plan_chunks(const MetaParams& a, MetaSmem& s) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -244,35 +243,46 @@ __device__ __forceinline__ void plan_chunks(const MetaParams& a, MetaSmem& s) {
             e[2] = t;
         }
     };
-    for (int b = lo; b < hi; ++b) {
-        const int64_t mine = request_cost(b);
+    s.cost[tid] = at;
+    __syncthreads();
+    // A thread places one cut: bisection over the threads' costs, the requests of that thread, then
+    // the row tiles by the closed form.
+    for (int64_t i = tid; i < a.parts && i * budget < total; i += kMetaThreads) {
+        const int64_t x64 = i * budget;
+        int t0 = 0, t1 = kMetaThreads;   // the last thread whose cost is <= x64
+        while (t1 - t0 > 1) {
+            const int mid = (t0 + t1) >> 1;
+            if (s.cost[mid] <= x64) t0 = mid; else t1 = mid;
+        }
+        int64_t c0 = s.cost[t0];
+        int b = t0 * per;
+        for (int64_t mine = request_cost(b); c0 + mine <= x64; mine = request_cost(b)) {   // x64 < total: it ends
+            c0 += mine;
+            ++b;
+        }
         int n, L;
         const int64_t cap = len_of(b, n, L);
         const double p = L > n ? (double)(L - n) : 0.0;
         const int64_t mt = ((int64_t)n * h + kTileRows - 1) / kTileRows;
-        // cuts i with at <= i * budget < at + mine
-        for (int64_t i = (at + budget - 1) / budget; i < a.parts && i * budget < at + mine; ++i) {
-            const double x = (double)(i * budget - at) * (1.0 / 256.0);
-            int64_t m0 = 0, m1 = mt;   // largest m with cost(m) <= x
-            while (m1 - m0 > 1) {
-                const int64_t mid = (m0 + m1) / 2;
-                if (units_cost((double)mid, p, (double)L, inv_h, a.causal) <= x) m0 = mid; else m1 = mid;
-            }
-            int64_t keys = unit_keys(L, n, h, (int)m0, a.causal);
-            if (keys > cap) keys = cap;
-            const int64_t tiles = (keys + kTileKeys - 1) / kTileKeys;
-            int64_t t = (int64_t)floor(x - units_cost((double)m0, p, (double)L, inv_h, a.causal) - kUnitCost);
-            if (t < kMinPiece) t = 0;
-            if (t > 0 && t + kMinPiece > tiles) {
-                t = 0;
-                ++m0;
-            }
-            if (m0 >= mt)
-                put(i, b + 1, 0, 0);
-            else
-                put(i, b, (int)m0, (int)t);
+        const double x = (double)(x64 - c0) * (1.0 / 256.0);
+        int64_t m0 = 0, m1 = mt;   // largest m with cost(m) <= x
+        while (m1 - m0 > 1) {
+            const int64_t mid = (m0 + m1) / 2;
+            if (units_cost((double)mid, p, (double)L, inv_h, a.causal) <= x) m0 = mid; else m1 = mid;
         }
-        at += mine;
+        int64_t keys = unit_keys(L, n, h, (int)m0, a.causal);
+        if (keys > cap) keys = cap;
+        const int64_t tiles = (keys + kTileKeys - 1) / kTileKeys;
+        int64_t t = (int64_t)floor(x - units_cost((double)m0, p, (double)L, inv_h, a.causal) - kUnitCost);
+        if (t < kMinPiece) t = 0;
+        if (t > 0 && t + kMinPiece > tiles) {
+            t = 0;
+            ++m0;
+        }
+        if (m0 >= mt)
+            put(i, b + 1, 0, 0);
+        else
+            put(i, b, (int)m0, (int)t);
     }
     // the cuts at and past the total cost
     for (int64_t i = (total + budget - 1) / budget + tid; i <= a.parts; i += kMetaThreads) put(i, a.bs, 0, 0);
