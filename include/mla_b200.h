@@ -436,7 +436,7 @@ MLA_API size_t mla_chunk_workspace_bytes(int32_t num_parts);
  *                  NaN too); the rows below L must be finite
  *   cu_seqlens     int32 [bs + 1], non-decreasing, within [0, num_tokens] (other values are clamped)
  *   chunk_plan, num_parts  from mla_build_chunk_metadata for the same lengths, h_q and causal
- *   out, lse       bf16 [num_tokens, h_q, 512] (32-byte aligned), fp32 [num_tokens, h_q] (written)
+ *   out, lse       bf16 [num_tokens, h_q, 512], fp32 [num_tokens, h_q] (written)
  *   workspace      at least mla_chunk_workspace_bytes(num_parts) bytes, 256-byte aligned; calls that
  *                  overlap on the GPU need one each
  * num_tokens * h_q below 2^31 - 256, else MLA_ERR_UNSUPPORTED.  The result does not depend on how

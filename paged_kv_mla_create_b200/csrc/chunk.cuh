@@ -66,18 +66,24 @@ constexpr int kHiBoxes = kChunks - kLoBoxes;
 constexpr int kOffQ = 0;                            // Q chunks 4..8
 constexpr int kOffK = kOffQ + kQHiBytes;
 constexpr int kOffP = kOffK + kKSlots * kKSlotBytes;
-constexpr int kOffX = kOffP + kPBytes;              // row-max exchange 2 x 256 floats; of two finished
+constexpr int kOffX = kOffP + kPBytes + 2 * kBox;   // row-max exchange 2 x 256 floats; of two finished
                                                     // units each: row sums 256, row maxima 64
+constexpr int kOffStage = kOffP + kPBytes;           // 16 KB: half of Q columns [0, 256) on its way to tensor
+                                                    // memory, or o on its way out (4 warps x 2 x 2 KB)
 constexpr int kUnitSums = 2 * kSoftmaxThreads, kUnitSumsStride = kSoftmaxThreads + kCtaRows;   // floats
 constexpr int kOffPSig = kOffX + 5120;              // leader: landing words of the peer's signals
-constexpr int kOffBar = kOffPSig + 256;             // words: P 0..7, V 8..11, K 12, 13, Q 14..17, S 18..25, O 26..29
+constexpr int kOffBar = kOffPSig + 256;             // words: P 0..7, V 8..11, K 12, 13, Q 14..17, S 18..25, O 26..29, Q high 30..33
 
 enum : int {
     kBarKFull = 0,                      // leader (slot, half): both CTAs' chunks 0..3 / 4..8 landed
     kBarKEmpty = kBarKFull + 2 * kKSlots,    // both (slot, half): the PV MMAs finished with chunks 0..3 / all
     kBarQKDone = kBarKEmpty + 2 * kKSlots,   // both (slot): the tile's S MMAs finished reading the slot
     kBarVFull = kBarQKDone + kKSlots,   // leader (slot, half): the pair's partner V of output block 0 / 1 landed
-    kBarQFull = kBarVFull + 2 * kKSlots,     // leader: Q landed / was written
+    kBarQFull = kBarVFull + 2 * kKSlots,     // leader: Q columns [0, 256) in tensor memory
+    kBarQHiFull,                        // leader: Q columns [256, 576) in shared memory
+    kBarQLo,                            // local: a half of Q columns [0, 256) landed in the staging area
+    kBarQHi,                            // local, 8-bit cache: Q columns [256, 576) landed as bf16
+    kBarStage,                          // local: the 4 Q warps are done with the staging area's content
     kBarQEmpty,                         // both: the unit's last S MMA finished (Q reusable)
     kBarSFull,                          // both (x2): S tile in tensor memory
     kBarSFree = kBarSFull + 2,          // leader (x2): 16 softmax warps have read S
@@ -244,7 +250,8 @@ template <int kKv>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap klo_map,
                  const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map,
-                 const __grid_constant__ Params p) {
+                 const __grid_constant__ CUtensorMap qlo_map, const __grid_constant__ CUtensorMap o_map,
+                 const __grid_constant__ CUtensorMap ps_map, const __grid_constant__ Params p) {
     constexpr bool kFp8 = kKv != 0;
     constexpr bool kE5M2 = kKv == 2;
     extern __shared__ uint8_t smem_raw[];
@@ -271,8 +278,11 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             mbar_init(bar(kBarQKDone + s), 1);
             mbar_init(bar(kBarKRaw + s), 1);
         }
-        // the Q TMA (bf16 cache) and the 4 warps that write Q
-        mbar_init(bar(kBarQFull), (kFp8 ? 0 : 1) + 4);
+        mbar_init(bar(kBarQFull), 4);
+        mbar_init(bar(kBarQHiFull), kFp8 ? 4 : 1);
+        mbar_init(bar(kBarQLo), 1);
+        mbar_init(bar(kBarQHi), 1);
+        mbar_init(bar(kBarStage), 4);
         mbar_init(bar(kBarQEmpty), 1);
         for (int j = 0; j < 2; ++j) {
             mbar_init(bar(kBarSFull + j), 1);
@@ -297,6 +307,9 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
         prefetch_tensormap(&klo_map);
         prefetch_tensormap(&v_map);
         prefetch_tensormap(&q_map);
+        prefetch_tensormap(&qlo_map);
+        prefetch_tensormap(&o_map);
+        prefetch_tensormap(&ps_map);
     }
     tc_fence_before();
     __syncthreads();
@@ -456,7 +469,9 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
     } else if (warp >= kQWarp0 && warp < kQWarp0 + 4) {
         // ------------------------------------------------------------ Q, o (8-bit cache: and partner V)
         // These warps bring a unit's Q, then write the result of the unit before while the softmax
-        // warps are at the new unit's first tile already.
+        // warps are at the new unit's first tile already.  Q columns [0, 256) pass through the staging
+        // area in two halves (a TMA load each, then shared -> registers -> tensor memory): by the time
+        // the unit before is done with Q, the first half is in registers and the second has landed.
         const int quarter = warp & 3;
         const int qt = threadIdx.x - kQWarp0 * 32;          // 0..127
         const int rloc = (32 * quarter + lane) & 63;
@@ -465,25 +480,78 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
         const int half = quarter >> 1;                      // lanes of O's columns [0, 128) / [128, 256) of a block
         const float dk = p.descale_k ? *p.descale_k : 1.0f;
         const float* xmax = reinterpret_cast<const float*>(smem + kOffX);
-        uint32_t uq = 0, g = 0, ue = 0;
+        const uint32_t stage = sbase + kOffStage;
+        const bool issuer = quarter == 3 && lane == 0;
+        uint32_t uq = 0, g = 0, ue = 0, nstage = 0;   // nstage: phases of kBarStage, three a unit
         bool q_range = false, alive = true;
         Unit u, done;
+        done.slot = done.row0 = done.nrows = 0;
+        auto all = [](bool ok) -> bool { return __all_sync(0xffffffffu, ok); };
+        // this warp is done with the staging area's content (1 of 4); the issuer goes on once all are.
+        // The fence holds back the arrival until the warp's loads have their data: the next TMA load
+        // would overwrite it (without the fence single units of Q came out as the next half's).
+        auto stage_read = [&]() -> bool {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarStage));
+            bool ok = true;
+            if (issuer) ok = mbar_wait_bounded(bar(kBarStage), nstage & 1u, actl);
+            ++nstage;
+            return all(ok);
+        };
+        auto q_load = [&](const Unit& v, int hb) {   // (issuer)
+            mbar_arrive_expect_tx(bar(kBarQLo), 2 * kBox);
+            tma_load_3d(stage, &qlo_map, bar(kBarQLo), 0, v.row0 + kCtaRows * (int)rank, 2 * hb);
+        };
+        // the row's 128 columns in the staging area (rows past the unit's last are other rows, or
+        // zeros past q: computed, never stored)
+        auto q_read = [&](uint4 (&v)[16]) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                v[k] = ld_shared_v4u(stage + (uint32_t)((k >> 3) * kBox + rloc * 128) + 16u * (((uint32_t)k & 7u) ^ ((uint32_t)rloc & 7u)));
+                if constexpr (kFp8) {
+                    const bool row = rtile < u.nrows;
+                    bool range = false;
+                    v[k].x = decode::bf16x2_to_f16x2(v[k].x, range);
+                    v[k].y = decode::bf16x2_to_f16x2(v[k].y, range);
+                    v[k].z = decode::bf16x2_to_f16x2(v[k].z, range);
+                    v[k].w = decode::bf16x2_to_f16x2(v[k].w, range);
+                    q_range |= range && row;
+                }
+            }
+        };
+        auto q_write = [&](const uint4 (&v)[16], int hb) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t w[16];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    w[4 * k] = v[4 * c + k].x;
+                    w[4 * k + 1] = v[4 * c + k].y;
+                    w[4 * k + 2] = v[4 * c + k].z;
+                    w[4 * k + 3] = v[4 * c + k].w;
+                }
+                tmem_st16(tmem + lane_off + kTmemQ + 64u * hb + 16u * c, w);
+            }
+        };
         // o (or the piece's fp32 partial, normalised) and lse of unit `done`: 32 tensor-memory columns
-        // at a time, each thread writing whole 32-byte sectors of its row (64 bytes of bf16, 128 of
-        // fp32): nothing is staged, no store is waited for.
+        // a step, 64 bytes of each of the warp's 32 rows a pass (bf16: one pass, fp32: two) through
+        // one of its two 2 KB staging buffers (64-byte swizzle: unit k of row r at k ^ ((r >> 1) & 3))
+        // out as a TMA box; a pass waits for the store before the last one to have read its buffer.
         auto epilogue = [&]() -> bool {
             const bool full = mbar_wait_bounded(bar(kBarOFull), ue & 1u, actl);
             const bool sums = mbar_wait_bounded(bar(kBarLx + (ue & 1u)), (ue >> 1) & 1u, actl);
-            if (!__all_sync(0xffffffffu, full && sums)) return false;
+            if (!all(full && sums)) return false;
             tc_fence_after();
             const float* x = xmax + kUnitSums + (ue & 1u) * kUnitSumsStride + rloc;
             const float l_run = (x[0] + x[64]) + (x[128] + x[192]);
             const float m_run = x[kSoftmaxThreads];
             const float inv = l_run > 0.f ? dk / l_run : 0.f;
             const float lse_val = l_run > 0.f ? (m_run + __log2f(l_run)) * 0.69314718055994531f : -INFINITY;
-            const bool direct = done.slot < 0, write = !direct || rtile < done.nrows;
-            __nv_bfloat16* const orow = p.out + ((int64_t)done.row0 + rtile) * kDv + 128 * half;
-            float* const prow = p.part_o + ((int64_t)done.slot * kTileRows + rtile) * kDv + 128 * half;
+            const bool direct = done.slot < 0;
+            const int r0 = kCtaRows * (int)rank + 32 * (quarter & 1);   // the warp's first row
+            const int rows = min(32, done.nrows - r0);                  // of its rows in the unit (<= 0: none)
+            uint32_t npass = 0;
 #pragma unroll 1
             for (int st = 0; st < 8; ++st) {
                 uint32_t raw[32];
@@ -495,23 +563,47 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                     tc_fence_before();
                     signal_leader(kBarOEmpty, 26 + quarter);   // O is free for the next unit
                 }
-                const int col = 256 * (st >> 2) + 32 * (st & 3);
-                if (write) {
+#pragma unroll
+                for (int pass = 0; pass < 2; ++pass) {
+                    if (direct && pass == 1) break;
+                    uint32_t w[16];
+                    int col = 256 * (st >> 2) + 128 * half + 32 * (st & 3);
                     if (direct) {
-                        uint32_t w[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k)
                             w[k] = pack_bf16x2(__uint_as_float(raw[2 * k]) * inv, __uint_as_float(raw[2 * k + 1]) * inv);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) st_global_v8(orow + col + 16 * k, w + 8 * k);
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) raw[k] = __float_as_uint(__uint_as_float(raw[k]) * inv);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) st_global_v8(prow + col + 8 * k, raw + 8 * k);
+                        for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(raw[16 * pass + k]) * inv);
+                        col += 16 * pass;
                     }
+                    const uint32_t buf = stage + 4096u * (uint32_t)quarter + 2048u * (npass & 1u);
+                    if (lane == 0 && npass >= 2) bulk_wait_read<1>();
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        st_shared_v4u(buf + 64u * (uint32_t)lane + 16u * ((uint32_t)k ^ (((uint32_t)lane >> 1) & 3u)), w[4 * k],
+                                      w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (!direct || rows == 32) {   // (a partial's slot always has room for a whole box)
+                        if (lane == 0) {
+                            if (direct)
+                                tma_store_2d(&o_map, buf, col, done.row0 + r0);
+                            else
+                                tma_store_2d(&ps_map, buf, col, done.slot * kTileRows + r0);
+                            bulk_commit();
+                        }
+                    } else {
+                        // the rows behind belong to another request or to nobody
+                        for (int r = lane >> 2; r < rows; r += 8) {
+                            const uint4 v = ld_shared_v4u(buf + 64u * (uint32_t)r + 16u * (((uint32_t)lane & 3u) ^ (((uint32_t)r >> 1) & 3u)));
+                            *reinterpret_cast<uint4*>(p.out + ((int64_t)done.row0 + r0 + r) * kDv + col + 8 * (lane & 3)) = v;
+                        }
+                    }
+                    ++npass;
+                    __syncwarp();
                 }
-                __syncwarp();
             }
             if (half == 0) {
                 if (!direct)
@@ -519,98 +611,81 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 else if (rtile < done.nrows)
                     p.lse[(int64_t)done.row0 + rtile] = lse_val;
             }
+            if (lane == 0) bulk_wait_read<0>();   // the staging area is free again
             ++ue;
             return true;
         };
-        while (alive && iter.next_tiles(p, u)) {
-            const int n = u.tiles();
-            // ---- Q of the unit (rows past its last repeat it: computed, never stored): columns
-            // [256, 576) into shared memory, columns [0, 256) into tensor memory, each row twice
-            // (lane r and 64 + r).  The first half's loads go out before the unit before is done
-            // with Q.
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)u.row0 + min(rtile, u.nrows - 1)) * kDqk);
+        bool more = iter.next_tiles(p, u);
+        if (more && issuer) q_load(u, 0);
+        while (more) {
+            // ---- Q of the unit
             uint4 v[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = __ldg(src + k);
-            const bool free = uq == 0 || mbar_wait_bounded(bar(kBarQEmpty), (uq - 1) & 1u, actl);
-            if (!__all_sync(0xffffffffu, free)) break;
+            if (!all(mbar_wait_bounded(bar(kBarQLo), 0u, actl))) break;
+            q_read(v);
+            if (!stage_read()) break;
+            if (issuer) q_load(u, 1);
+            if (!all(uq == 0 || mbar_wait_bounded(bar(kBarQEmpty), (uq - 1) & 1u, actl))) break;
             tc_fence_after();
-            if (!kFp8 && quarter == 3 && lane == 0) {
-                if (leader) mbar_arrive_expect_tx(bar(kBarQFull), 2 * kQHiBytes);
-                tma_load_3d_pair(sbase + kOffQ, &q_map, map_to_cta(bar(kBarQFull), 0), 0,
-                                 u.row0 + kCtaRows * (int)rank, kQLoChunks);
+            if (issuer) {   // columns [256, 576): where S reads them (8-bit cache: converted in place first)
+                if constexpr (kFp8) {
+                    mbar_arrive_expect_tx(bar(kBarQHi), kQHiBytes);
+                    tma_load_3d(sbase + kOffQ, &q_map, bar(kBarQHi), 0, u.row0 + kCtaRows * (int)rank, kQLoChunks);
+                } else {
+                    if (leader) mbar_arrive_expect_tx(bar(kBarQHiFull), 2 * kQHiBytes);
+                    tma_load_3d_pair(sbase + kOffQ, &q_map, map_to_cta(bar(kBarQHiFull), 0), 0,
+                                     u.row0 + kCtaRows * (int)rank, kQLoChunks);
+                }
             }
             __syncwarp();
-#pragma unroll
-            for (int hb = 0; hb < 2; ++hb) {
-                if (hb == 1) {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = __ldg(src + 16 + k);
-                }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        w[4 * k] = v[4 * c + k].x;
-                        w[4 * k + 1] = v[4 * c + k].y;
-                        w[4 * k + 2] = v[4 * c + k].z;
-                        w[4 * k + 3] = v[4 * c + k].w;
-                    }
-                    if constexpr (kFp8) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) w[k] = decode::bf16x2_to_f16x2(w[k], q_range);
-                    }
-                    tmem_st16(tmem + lane_off + kTmemQ + 64u * hb + 16u * c, w);
-                }
-            }
-            if constexpr (kFp8) {
-                // Q columns [256, 576) as f16 (128-byte swizzle): lane quarters 0 / 1 take chunks
-                // 0..2 of them, quarters 2 / 3 chunks 3..4
-                const int c0 = quarter < 2 ? 0 : 3, c1 = quarter < 2 ? 3 : kQHiChunks;
-#pragma unroll 1
-                for (int cc = c0; cc < c1; ++cc) {
-                    const uint32_t qrow = sbase + kOffQ + cc * kBox + (uint32_t)rloc * 128u;
-                    uint4 x[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] = __ldg(src + 32 + 8 * cc + k);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        st_shared_v4u(qrow + 16u * ((uint32_t)k ^ ((uint32_t)rloc & 7u)),
-                                      decode::bf16x2_to_f16x2(x[k].x, q_range), decode::bf16x2_to_f16x2(x[k].y, q_range),
-                                      decode::bf16x2_to_f16x2(x[k].z, q_range), decode::bf16x2_to_f16x2(x[k].w, q_range));
-                }
-                fence_proxy_async_smem();
-                if (__any_sync(0xffffffffu, q_range) && lane == 0) raise_error(32 /* MLA_DEVERR_Q_RANGE */);
-                __syncwarp();
-            }
+            q_write(v, 0);
+            if (!all(mbar_wait_bounded(bar(kBarQLo), 1u, actl))) break;
+            q_read(v);
+            if (!stage_read()) break;
+            q_write(v, 1);
             tc_wait_st();
             tc_fence_before();
             signal_leader(kBarQFull, 14 + quarter);
-            {
-                // the unit after this one: its query rows into L2
-                UnitIter peek = iter;
-                Unit nu;
-                if (peek.next_tiles(p, nu) && rtile < nu.nrows) {
-                    const uint8_t* row = reinterpret_cast<const uint8_t*>(p.q + ((int64_t)nu.row0 + rtile) * kDqk);
-                    for (int k = half; k < 9; k += 2) prefetch_l2(row + 128 * k);
+            if constexpr (kFp8) {
+                if (!all(mbar_wait_bounded(bar(kBarQHi), uq & 1u, actl))) break;
+                // bf16 -> f16 in place: 16-byte unit qt + 128 j of the 64 rows x 5 chunks x 8 units
+#pragma unroll 4
+                for (int j = 0; j < 20; ++j) {
+                    const uint32_t at = sbase + kOffQ + 16u * (uint32_t)(qt + 128 * j);
+                    uint4 x = ld_shared_v4u(at);
+                    bool range = false;
+                    x.x = decode::bf16x2_to_f16x2(x.x, range);
+                    x.y = decode::bf16x2_to_f16x2(x.y, range);
+                    x.z = decode::bf16x2_to_f16x2(x.z, range);
+                    x.w = decode::bf16x2_to_f16x2(x.w, range);
+                    st_shared_v4u(at, x.x, x.y, x.z, x.w);
+                    q_range |= range && kCtaRows * (int)rank + (((qt + 128 * j) >> 3) & 63) < u.nrows;
                 }
+                fence_proxy_async_smem();
+                signal_leader(kBarQHiFull, 30 + quarter);
+                if (__any_sync(0xffffffffu, q_range) && lane == 0) raise_error(32 /* MLA_DEVERR_Q_RANGE */);
+                __syncwarp();
             }
+            // ---- the unit before: its result
+            if (!all(mbar_wait_bounded(bar(kBarStage), (nstage - 1) & 1u, actl))) break;   // every warp has read its Q
             if (uq > 0 && !epilogue()) break;
             done = u;
             ++uq;
+            const Unit cur = u;
+            more = iter.next_tiles(p, u);
+            if (!stage_read()) break;
+            if (more && issuer) q_load(u, 0);
             if constexpr (kFp8) {
                 // ---- partner V of each tile: 4 chunks x 64 rows x 4 sixteen-byte units of 8-bit
                 // values, 8 per thread, widened to f16 on the way into the slot once the tile's S
                 // MMAs are done, rows at or past L as zeros
-                const int32_t* bt_row = p.block_table + (int64_t)u.b * p.bt_stride;
-                for (int i = 0; i < n; ++i, ++g) {
-                    const int blk = 2 * (u.t0 + i) + 1 - (int)rank;
-                    int pg = blk < u.kb1 ? __ldg(bt_row + blk) : -1;
+                const int32_t* bt_row = p.block_table + (int64_t)cur.b * p.bt_stride;
+                for (int i = 0; i < cur.tiles(); ++i, ++g) {
+                    const int blk = 2 * (cur.t0 + i) + 1 - (int)rank;
+                    int pg = blk < cur.kb1 ? __ldg(bt_row + blk) : -1;
                     if (pg < 0 || (int64_t)pg >= p.num_pages) pg = -1;   // reported by the K loads
                     const int s = (int)(g & 1u);
                     const uint32_t slot = sbase + kOffK + s * kKSlotBytes;
-                    const int valid = u.L - blk * kPage;
+                    const int valid = cur.L - blk * kPage;
                     uint4 w[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -622,7 +697,7 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                     }
                     const bool s_done = mbar_wait_bounded(bar(kBarQKDone + s), (g >> 1) & 1u, actl);
                     if (!__all_sync(0xffffffffu, s_done)) {
-                        alive = false;
+                        alive = more = false;
                         break;
                     }
 #pragma unroll
@@ -646,6 +721,7 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             }
         }
         if (alive && ue < uq) epilogue();
+        if (lane == 0) bulk_wait<0>();   // the stores
         drain_on_abort();
     } else if (warp == 1) {
         // ------------------------------------------------------------ S issuer (leader)
@@ -676,7 +752,7 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                         for (int kk = 0; kk < 4; ++kk)
                             mma_pair_ts(d, tmem + kTmemQ + 32u * c + 8u * kk, smem_desc_sw128(slot + c * kBox + 32u * kk, 16, 1024),
                                         kFp8 ? kIdescQK16 : kIdescQK, (c | kk) ? 1u : 0u);
-                    if (!wait(kBarKFull + 2 * s + 1, (g >> 1) & 1u)) {
+                    if ((i == 0 && !wait(kBarQHiFull, uq & 1u)) || !wait(kBarKFull + 2 * s + 1, (g >> 1) & 1u)) {
                         alive = false;
                         break;
                     }
