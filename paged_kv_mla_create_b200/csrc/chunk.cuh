@@ -69,7 +69,7 @@ constexpr int kOffP = kOffK + kKSlots * kKSlotBytes;
 constexpr int kOffX = kOffP + kPBytes + 2 * kBox;   // row-max exchange 2 x 256 floats; of two finished
                                                     // units each: row sums 256, row maxima 64
 constexpr int kOffStage = kOffP + kPBytes;           // 16 KB: half of Q columns [0, 256) on its way to tensor
-                                                    // memory, or o on its way out (4 warps x 2 x 2 KB)
+                                                    // memory, or o on its way out (4 warps x 4 KB)
 constexpr int kUnitSums = 2 * kSoftmaxThreads, kUnitSumsStride = kSoftmaxThreads + kCtaRows;   // floats
 constexpr int kOffPSig = kOffX + 5120;              // leader: landing words of the peer's signals
 constexpr int kOffBar = kOffPSig + 256;             // words: P 0..7, V 8..11, K 12, 13, Q 14..17, S 18..25, O 26..29, Q high 30..33
@@ -250,8 +250,7 @@ template <int kKv>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap klo_map,
                  const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map,
-                 const __grid_constant__ CUtensorMap qlo_map, const __grid_constant__ CUtensorMap o_map,
-                 const __grid_constant__ CUtensorMap ps_map, const __grid_constant__ Params p) {
+                 const __grid_constant__ CUtensorMap qlo_map, const __grid_constant__ Params p) {
     constexpr bool kFp8 = kKv != 0;
     constexpr bool kE5M2 = kKv == 2;
     extern __shared__ uint8_t smem_raw[];
@@ -308,8 +307,6 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
         prefetch_tensormap(&v_map);
         prefetch_tensormap(&q_map);
         prefetch_tensormap(&qlo_map);
-        prefetch_tensormap(&o_map);
-        prefetch_tensormap(&ps_map);
     }
     tc_fence_before();
     __syncthreads();
@@ -534,10 +531,11 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 tmem_st16(tmem + lane_off + kTmemQ + 64u * hb + 16u * c, w);
             }
         };
-        // o (or the piece's fp32 partial, normalised) and lse of unit `done`: 32 tensor-memory columns
-        // a step, 64 bytes of each of the warp's 32 rows a pass (bf16: one pass, fp32: two) through
-        // one of its two 2 KB staging buffers (64-byte swizzle: unit k of row r at k ^ ((r >> 1) & 3))
-        // out as a TMA box; a pass waits for the store before the last one to have read its buffer.
+        // o (or the piece's fp32 partial, normalised) and lse of unit `done`: 64 tensor-memory columns
+        // a step, 128 bytes of each of the warp's 32 rows a pass (bf16: one pass, fp32: two), turned in
+        // 4 KB of the staging area (16-byte unit k of row r at k ^ (r & 7)) so that 8 lanes write a
+        // whole line.  (A unit's 64 KB in 32-column steps: ~4,400 cycles as 32-byte stores straight
+        // from the registers, one line each; ~5,200 as TMA boxes of 2 KB, two in flight a warp.)
         auto epilogue = [&]() -> bool {
             const bool full = mbar_wait_bounded(bar(kBarOFull), ue & 1u, actl);
             const bool sums = mbar_wait_bounded(bar(kBarLx + (ue & 1u)), (ue >> 1) & 1u, actl);
@@ -550,59 +548,55 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             const float lse_val = l_run > 0.f ? (m_run + __log2f(l_run)) * 0.69314718055994531f : -INFINITY;
             const bool direct = done.slot < 0;
             const int r0 = kCtaRows * (int)rank + 32 * (quarter & 1);   // the warp's first row
-            const int rows = min(32, done.nrows - r0);                  // of its rows in the unit (<= 0: none)
-            uint32_t npass = 0;
+            const int rows = direct ? min(32, done.nrows - r0) : 32;    // rows to write (<= 0: none)
+            const uint32_t buf = stage + 4096u * (uint32_t)quarter;
+            const int rsub = lane >> 3, unit = lane & 7;                // store: row 4 j + rsub, 16-byte unit
+            uint8_t* const dst = direct ? reinterpret_cast<uint8_t*>(p.out + ((int64_t)done.row0 + r0) * kDv)
+                                        : reinterpret_cast<uint8_t*>(p.part_o + ((int64_t)done.slot * kTileRows + r0) * kDv);
+            const int esize = direct ? 2 : 4;
+            const int nst = direct ? 4 : 8;   // passes of 128 bytes a row: 64 bf16 columns, or 32 fp32
 #pragma unroll 1
-            for (int st = 0; st < 8; ++st) {
-                uint32_t raw[32];
-                const uint32_t src = tmem + lane_off + kTmemO + 32u * st;
-                tmem_ld16(src, *reinterpret_cast<uint32_t(*)[16]>(raw));
-                tmem_ld16(src + 16u, *reinterpret_cast<uint32_t(*)[16]>(raw + 16));
-                tc_wait_ld();
-                if (st == 7) {
+            for (int st = 0; st < nst; ++st) {
+                const int c0 = direct ? 64 * st : 32 * st;   // tensor-memory column
+                __syncwarp();   // the pass before has been read
+#pragma unroll
+                for (int hp = 0; hp < 2; ++hp) {
+                    if (!direct && hp == 1) break;
+                    uint32_t raw[32];
+                    tmem_ld16(tmem + lane_off + kTmemO + (uint32_t)(c0 + 32 * hp), *reinterpret_cast<uint32_t(*)[16]>(raw));
+                    tmem_ld16(tmem + lane_off + kTmemO + (uint32_t)(c0 + 32 * hp) + 16u, *reinterpret_cast<uint32_t(*)[16]>(raw + 16));
+                    tc_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) raw[k] = __float_as_uint(__uint_as_float(raw[k]) * inv);
+                    if (direct) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) raw[k] = pack_bf16x2(__uint_as_float(raw[2 * k]), __uint_as_float(raw[2 * k + 1]));
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (direct && k >= 4) break;
+                        const uint32_t unit_at = (uint32_t)(k + 4 * hp) ^ ((uint32_t)lane & 7u);
+                        st_shared_v4u(buf + 128u * (uint32_t)lane + 16u * unit_at, raw[4 * k], raw[4 * k + 1], raw[4 * k + 2], raw[4 * k + 3]);
+                    }
+                }
+                if (st == nst - 1) {
                     tc_fence_before();
                     signal_leader(kBarOEmpty, 26 + quarter);   // O is free for the next unit
                 }
+                __syncwarp();
+                const int col = 256 * (c0 >> 7) + 128 * half + (c0 & 127);
+                // (rows behind the unit's last belong to another request or to nobody)
 #pragma unroll
-                for (int pass = 0; pass < 2; ++pass) {
-                    if (direct && pass == 1) break;
-                    uint32_t w[16];
-                    int col = 256 * (st >> 2) + 128 * half + 32 * (st & 3);
-                    if (direct) {
+                for (int j4 = 0; j4 < 8; j4 += 4) {
+                    uint4 v[4];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            w[k] = pack_bf16x2(__uint_as_float(raw[2 * k]) * inv, __uint_as_float(raw[2 * k + 1]) * inv);
-                    } else {
+                    for (int j = 0; j < 4; ++j)
+                        v[j] = ld_shared_v4u(buf + 128u * (uint32_t)(4 * (j4 + j) + rsub) +
+                                             16u * ((uint32_t)unit ^ ((uint32_t)(4 * (j4 + j) + rsub) & 7u)));
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(raw[16 * pass + k]) * inv);
-                        col += 16 * pass;
-                    }
-                    const uint32_t buf = stage + 4096u * (uint32_t)quarter + 2048u * (npass & 1u);
-                    if (lane == 0 && npass >= 2) bulk_wait_read<1>();
-                    __syncwarp();
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        st_shared_v4u(buf + 64u * (uint32_t)lane + 16u * ((uint32_t)k ^ (((uint32_t)lane >> 1) & 3u)), w[4 * k],
-                                      w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (!direct || rows == 32) {   // (a partial's slot always has room for a whole box)
-                        if (lane == 0) {
-                            if (direct)
-                                tma_store_2d(&o_map, buf, col, done.row0 + r0);
-                            else
-                                tma_store_2d(&ps_map, buf, col, done.slot * kTileRows + r0);
-                            bulk_commit();
-                        }
-                    } else {
-                        // the rows behind belong to another request or to nobody
-                        for (int r = lane >> 2; r < rows; r += 8) {
-                            const uint4 v = ld_shared_v4u(buf + 64u * (uint32_t)r + 16u * (((uint32_t)lane & 3u) ^ (((uint32_t)r >> 1) & 3u)));
-                            *reinterpret_cast<uint4*>(p.out + ((int64_t)done.row0 + r0 + r) * kDv + col + 8 * (lane & 3)) = v;
-                        }
-                    }
-                    ++npass;
-                    __syncwarp();
+                    for (int j = 0; j < 4; ++j)
+                        if (4 * (j4 + j) + rsub < rows)
+                            *reinterpret_cast<uint4*>(dst + ((int64_t)(4 * (j4 + j) + rsub) * kDv + col) * esize + 16 * unit) = v[j];
                 }
             }
             if (half == 0) {
@@ -611,7 +605,6 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 else if (rtile < done.nrows)
                     p.lse[(int64_t)done.row0 + rtile] = lse_val;
             }
-            if (lane == 0) bulk_wait_read<0>();   // the staging area is free again
             ++ue;
             return true;
         };
@@ -721,7 +714,6 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             }
         }
         if (alive && ue < uq) epilogue();
-        if (lane == 0) bulk_wait<0>();   // the stores
         drain_on_abort();
     } else if (warp == 1) {
         // ------------------------------------------------------------ S issuer (leader)

@@ -723,9 +723,9 @@ mla_status_t mla_chunk_paged(const void* q, int32_t q_dtype, int32_t num_tokens,
     // Tensor maps, as mla_decode_paged's: K pages as 64-column chunks (bf16: 0..3 and
     // 4..8 apart; 8-bit: all nine), V as two-chunk boxes, q
     // rows (64 columns, rows, 9 chunks) in boxes of 64 rows x columns [256, 576) and x 128 of the columns
-    // below, o rows and partial rows as 32-row x 64-byte boxes (64-byte swizzle).
+    // below.
     const int32_t rows = num_tokens * h_q;
-    CUtensorMap k_map, klo_map, v_map, q_map, qlo_map, o_map, ps_map;
+    CUtensorMap k_map, klo_map, v_map, q_map, qlo_map;
     const cuuint64_t pool_rows = (cuuint64_t)num_pages * 64;
     const cuuint32_t es[3] = {1, 1, 1};
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -738,12 +738,6 @@ mla_status_t mla_chunk_paged(const void* q, int32_t q_dtype, int32_t num_tokens,
         return encode(m, type, 3, const_cast<void*>(base), dim, stride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
-    auto map2 = [&](CUtensorMap* m, CUtensorMapDataType type, void* base, cuuint64_t n, cuuint64_t size) {
-        const cuuint64_t dim[2] = {512, n}, stride[1] = {512 * size};
-        const cuuint32_t box[2] = {(cuuint32_t)(64 / size), 32};
-        return encode(m, type, 2, base, dim, stride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-                      CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-    };
     bool ok;
     if (kv_dtype == MLA_DTYPE_BF16) {
         ok = map3(&k_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, k_cache, pool_rows, 1152, 128, 64, kHiBoxes, CU_TENSOR_MAP_SWIZZLE_128B) &&
@@ -754,9 +748,7 @@ mla_status_t mla_chunk_paged(const void* q, int32_t q_dtype, int32_t num_tokens,
         klo_map = v_map = k_map;   // the 8-bit path loads whole pages, and the partner's V through registers
     }
     ok = ok && map3(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, (cuuint64_t)rows, 1152, 128, 64, kQHiChunks, CU_TENSOR_MAP_SWIZZLE_128B) &&
-         map3(&qlo_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, (cuuint64_t)rows, 1152, 128, 64, 2, CU_TENSOR_MAP_SWIZZLE_128B) &&
-         map2(&o_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, (cuuint64_t)rows, 2) &&
-         map2(&ps_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, part_o, (cuuint64_t)num_parts * 2 * kTileRows, 4);
+         map3(&qlo_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, (cuuint64_t)rows, 1152, 128, 64, 2, CU_TENSOR_MAP_SWIZZLE_128B);
     if (!ok) return MLA_ERR_CUDA;
 
     Params p;
@@ -797,7 +789,7 @@ mla_status_t mla_chunk_paged(const void* q, int32_t q_dtype, int32_t num_tokens,
     cfg.numAttrs = 1;
     auto kernel = kv_dtype == MLA_DTYPE_BF16 ? mla_chunk_kernel<0>
                   : (kv_dtype == MLA_DTYPE_FP8_E4M3 ? mla_chunk_kernel<1> : mla_chunk_kernel<2>);
-    if (cudaLaunchKernelEx(&cfg, kernel, k_map, klo_map, v_map, q_map, qlo_map, o_map, ps_map, p) != cudaSuccess) return MLA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, k_map, klo_map, v_map, q_map, qlo_map, p) != cudaSuccess) return MLA_ERR_CUDA;
     // the merge of the units that the plan cut: scheduled early, it waits on the device
     cfg.gridDim = dim3(kMergeCtasPerPart * num_parts);
     cfg.blockDim = dim3(kMergeThreads);
