@@ -19,7 +19,9 @@ The three entry points follow the calls of the SGLang FlashMLA attention backend
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -114,12 +116,36 @@ def _check(status: int, what: str):
         raise MlaError(status, what)
 
 
-def _stream(device: torch.device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _stream(device) -> ctypes.c_void_p:
+    """The device's current stream (device: a torch.device or an index), without a Stream object."""
+    index = device if isinstance(device, int) else device.index
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index))
 
 
 def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+
+
+def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
+    """A tensor's address as the plain number that ctypes takes for a pointer (cheaper than an object)."""
+    return t.data_ptr() if t is not None else None
+
+
+@functools.lru_cache(maxsize=None)
+def _device_parts(index: int) -> int:
+    """num_chunk_parts of a device."""
+    return num_chunk_parts(sm_count(index))
+
+
+def _on(device: torch.device):
+    """A context with `device` current, or none where it is already (the switch costs microseconds)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _same_device(device: torch.device, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("all tensors must be on the same CUDA device")
 
 
 def _require_cuda(*tensors):
@@ -444,32 +470,33 @@ def build_chunk_metadata(req_to_token: torch.Tensor, req_pool_indices: torch.Ten
     taken from the list, in request order, and the new slots entered into req_to_token (the
     requests' rows must differ then).  Rows behind the last request get position 0 and slot
     pad_slot when fill_tail (-1: not a slot; set_kv_buffer skips and reports it), else nothing."""
-    _require_cuda(req_to_token, req_pool_indices, prefix_lens, chunk_lens, free_pages)
+    if not req_to_token.is_cuda:
+        raise ValueError("paged_kv_mla_create_b200 runs on CUDA tensors only")
+    dev = req_to_token.device
+    _same_device(dev, req_pool_indices, prefix_lens, chunk_lens, free_pages, *(out or ()))
     if req_to_token.dtype != torch.int32 or req_to_token.dim() != 2 or req_to_token.stride(1) != 1:
         raise ValueError("req_to_token must be a row-major int32 matrix")
     if num_tokens < 0 or max_seqlen_pad < 0 or num_heads <= 0:
         raise ValueError("num_tokens and max_seqlen_pad must not be negative, num_heads must be positive")
-    bs = int(req_pool_indices.shape[0])
-    for name, t in (("req_pool_indices", req_pool_indices), ("prefix_lens", prefix_lens), ("chunk_lens", chunk_lens)):
-        if t.dim() != 1 or t.shape[0] != bs:
-            raise ValueError(f"{name} must be a vector of one entry per request")
+    bs = req_pool_indices.shape[0]
+    if not (tuple(req_pool_indices.shape) == tuple(prefix_lens.shape) == tuple(chunk_lens.shape) == (bs,)):
+        raise ValueError("req_pool_indices, prefix_lens and chunk_lens must be vectors of one entry per request")
     if prefix_lens.dtype != chunk_lens.dtype:
         raise ValueError("prefix_lens and chunk_lens must have the same dtype")
-    dev = req_to_token.device
     rpi, pl, cl = req_pool_indices.contiguous(), prefix_lens.contiguous(), chunk_lens.contiguous()
     if free_pages is not None:
         if free_pages.dim() != 1 or free_pages.dtype != rpi.dtype:
             raise ValueError("free_pages must be a vector of req_pool_indices' dtype")
         free_pages = free_pages.contiguous()
-    for t in (rpi, pl, cl, free_pages, *(out or ())):
-        if t is not None and t.device != dev:
-            raise ValueError("all tensors must be on the same device")
-    with torch.cuda.device(dev):
-        parts = int(num_parts) if num_parts is not None else num_chunk_parts(sm_count(dev))
-        if out is None:
-            new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)
-            out = (new(bs, max_seqlen_pad), new(bs), new(bs + 1), new(num_tokens), new(num_tokens), new(parts, 8),
-                   new(1) if free_pages is not None else None)
+    parts = _device_parts(dev.index) if num_parts is None else int(num_parts)
+    if out is None:
+        # one allocation for all of them, the plan (16-byte aligned) first
+        sizes = (8 * max(parts, 0), bs * max_seqlen_pad, bs, bs + 1, num_tokens, num_tokens, 1)
+        plan, bt, seqlens, cu, positions, loc, taken = torch.empty(
+            sum(sizes), dtype=torch.int32, device=dev).split_with_sizes(sizes)
+        out = (bt.view(bs, max_seqlen_pad), seqlens, cu, positions, loc, plan.view(max(parts, 0), 8),
+               taken if free_pages is not None else None)
+    else:
         bt, seqlens, cu, positions, loc, plan, taken = out
         if bt.dtype != torch.int32 or bt.dim() != 2 or bt.stride(1) != 1 or bt.shape[0] < bs or bt.shape[1] < max_seqlen_pad:
             raise ValueError("block_table must be a row-major int32 [bs, max_seqlen_pad] matrix")
@@ -480,14 +507,16 @@ def build_chunk_metadata(req_to_token: torch.Tensor, req_pool_indices: torch.Ten
         _int32_vector(plan, "chunk_plan", 8 * parts)
         if taken is not None:
             _int32_vector(taken, "pages_taken", 1)
-        # a free list without entries is still a list (its data pointer may be null)
-        free_ptr = None if free_pages is None else ctypes.c_void_p(free_pages.data_ptr() or rpi.data_ptr())
+    bt, taken = out[0], out[6]
+    # a free list without entries is still a list (its data pointer may be null)
+    free_ptr = None if free_pages is None else free_pages.data_ptr() or rpi.data_ptr()
+    with _on(dev):
         _check(library().mla_build_chunk_metadata(
-            _ptr(req_to_token), req_to_token.shape[0], req_to_token.stride(0), _ptr(rpi), _index_dtype(rpi), _ptr(pl),
-            _ptr(cl), _index_dtype(pl), bs, int(num_tokens), free_ptr, free_pages.numel() if free_pages is not None else 0,
-            int(num_heads), int(bool(causal)), parts, _ptr(bt), bt.stride(0), int(max_seqlen_pad), PAGE_SIZE,
-            int(bool(fill_tail)), int(pad_slot), _ptr(seqlens), _ptr(cu), _ptr(positions), _ptr(loc), _ptr(plan),
-            _ptr(taken), _stream(dev)), "mla_build_chunk_metadata")
+            _addr(req_to_token), req_to_token.shape[0], req_to_token.stride(0), _addr(rpi), _index_dtype(rpi), _addr(pl),
+            _addr(cl), _index_dtype(pl), bs, int(num_tokens), free_ptr, free_pages.shape[0] if free_pages is not None else 0,
+            int(num_heads), int(bool(causal)), parts, _addr(bt), bt.stride(0), int(max_seqlen_pad), PAGE_SIZE,
+            int(bool(fill_tail)), int(pad_slot), _addr(seqlens), _addr(cu), _addr(positions), _addr(loc), _addr(plan),
+            _addr(taken), _stream(dev)), "mla_build_chunk_metadata")
     return out
 
 
@@ -502,7 +531,10 @@ def mla_chunk_paged(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.T
     build_chunk_metadata gives them for h_q heads and the same causal; k_cache bf16, float8_e4m3fn or
     float8_e5m2.  Returns (o bf16 [num_tokens, h_q, 512], lse fp32 [num_tokens, h_q]); rows of no
     request keep what out / lse held."""
-    _require_cuda(q, k_cache, block_table, cache_seqlens, cu_seqlens, chunk_plan, descale_q, descale_k, out, lse, workspace)
+    if not q.is_cuda:
+        raise ValueError("paged_kv_mla_create_b200 runs on CUDA tensors only")
+    dev = q.device
+    _same_device(dev, k_cache, block_table, cache_seqlens, cu_seqlens, chunk_plan, descale_q, descale_k, out, lse, workspace)
     if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 [num_tokens, h_q, head_dim] tensor")
     num_tokens, h_q, head_dim = (int(x) for x in q.shape)
@@ -522,17 +554,13 @@ def mla_chunk_paged(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.T
     for name, d in (("descale_q", descale_q), ("descale_k", descale_k)):
         if d is not None and (d.dtype != torch.float32 or d.numel() < 1):
             raise ValueError(f"{name} must be a float32 tensor of one element")
-    dev = q.device
-    for t in (k_cache, block_table, cache_seqlens, cu_seqlens, chunk_plan, descale_q, descale_k, out, lse, workspace):
-        if t is not None and t.device != dev:
-            raise ValueError("all tensors must be on the same device")
     if out is not None and (out.dtype != torch.bfloat16 or not out.is_contiguous()
                             or tuple(out.shape) != (num_tokens, h_q, head_dim_v)):
         raise ValueError("out must be a contiguous bf16 [num_tokens, h_q, head_dim_v] tensor")
     if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or tuple(lse.shape) != (num_tokens, h_q)):
         raise ValueError("lse must be a contiguous float32 [num_tokens, h_q] tensor")
     parts = int(chunk_plan.shape[0])
-    with torch.cuda.device(dev):
+    with _on(dev):
         if out is None:
             out = torch.empty((num_tokens, h_q, head_dim_v), dtype=torch.bfloat16, device=dev)
         if lse is None:
@@ -540,11 +568,11 @@ def mla_chunk_paged(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.T
         if workspace is None:
             workspace = torch.empty((chunk_workspace_bytes(parts),), dtype=torch.uint8, device=dev)
         _check(library().mla_chunk_paged(
-            _ptr(q), DTYPE_BF16, num_tokens, h_q, head_dim, int(head_dim_v), _ptr(k_cache), _CACHE_DTYPES[k_cache.dtype],
-            k_cache.numel() // (PAGE_SIZE * head_dim), PAGE_SIZE, _ptr(block_table), block_table.stride(0),
-            int(block_table.shape[1]), _ptr(cache_seqlens), _ptr(cu_seqlens), bs, _ptr(chunk_plan), parts,
-            float(softmax_scale), int(bool(causal)), _ptr(descale_q), _ptr(descale_k), _ptr(out), _ptr(lse),
-            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(dev)), "mla_chunk_paged")
+            _addr(q), DTYPE_BF16, num_tokens, h_q, head_dim, int(head_dim_v), _addr(k_cache), _CACHE_DTYPES[k_cache.dtype],
+            k_cache.numel() // (PAGE_SIZE * head_dim), PAGE_SIZE, _addr(block_table), block_table.stride(0),
+            int(block_table.shape[1]), _addr(cache_seqlens), _addr(cu_seqlens), bs, _addr(chunk_plan), parts,
+            float(softmax_scale), int(bool(causal)), _addr(descale_q), _addr(descale_k), _addr(out), _addr(lse),
+            _addr(workspace), workspace.numel() * workspace.element_size(), _stream(dev)), "mla_chunk_paged")
     return out, lse
 
 
