@@ -235,14 +235,12 @@ __device__ __forceinline__ void widen_chunk_rows(uint32_t src, uint32_t dst, int
     __syncwarp();
 }
 
-// Clear rows [valid, 64) of the four V chunks at slot positions 4n + c, + 1 (n = 0, 1).
+// Clear rows [valid, 64) of the four V chunks at slot positions 4n + c, + 1 (n = 0, 1): a lane a 16-byte
+// unit of every row.
 __device__ __forceinline__ void clear_v_rows(uint32_t slot, int c, int valid, int lane) {
-    if (valid < 0) valid = 0;
-    for (int x = lane; x < (kPage - valid) * 32; x += 32) {
-        const int row = valid + (x >> 5), k = x & 31;   // chunk k / 8, 16-byte unit k % 8
-        const int pos = 4 * (k >> 4) + c + ((k >> 3) & 1);
-        st_shared_v4u(slot + (uint32_t)(pos * kBox + row * 128 + 16 * (k & 7)), 0u, 0u, 0u, 0u);
-    }
+    const int pos = 4 * (lane >> 4) + c + ((lane >> 3) & 1);
+    const uint32_t unit = slot + (uint32_t)(pos * kBox + 16 * (lane & 7));
+    for (int row = max(valid, 0); row < kPage; ++row) st_shared_v4u(unit + 128u * (uint32_t)row, 0u, 0u, 0u, 0u);
 }
 
 // kKv: the cache's element type, 0 bf16, 1 e4m3, 2 e5m2 (8-bit caches are widened to f16).
