@@ -478,7 +478,8 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
         const uint32_t stage = sbase + kOffStage;
         const bool issuer = quarter == 3 && lane == 0;
         uint32_t uq = 0, g = 0, ue = 0, nstage = 0;   // nstage: phases of kBarStage, three a unit
-        bool q_range = false, alive = true;
+        bool alive = true;
+        uint32_t q_top = 0;   // 8-bit cache: largest magnitudes of q (bf16 pairs)
         Unit u, done;
         done.slot = done.row0 = done.nrows = 0;
         auto all = [](bool ok) -> bool { return __all_sync(0xffffffffu, ok); };
@@ -498,6 +499,16 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             mbar_arrive_expect_tx(bar(kBarQLo), 2 * kBox);
             tma_load_3d(stage, &qlo_map, bar(kBarQLo), 0, v.row0 + kCtaRows * (int)rank, 2 * hb);
         };
+        // bf16 -> f16, keeping the largest magnitude of the unit's rows (past 65504 f16 has no value)
+        auto q_to_f16 = [&](uint4& x, bool row) {
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (row) q_top = __vmaxu2(q_top, w[k] & 0x7FFF7FFFu);
+                w[k] = pack_f16x2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+            }
+            x = make_uint4(w[0], w[1], w[2], w[3]);
+        };
         // the row's 128 columns in the staging area (rows past the unit's last are other rows, or
         // zeros past q: computed, never stored)
         auto q_read = [&](uint4 (&v)[16]) {
@@ -505,13 +516,7 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             for (int k = 0; k < 16; ++k) {
                 v[k] = ld_shared_v4u(stage + (uint32_t)((k >> 3) * kBox + rloc * 128) + 16u * (((uint32_t)k & 7u) ^ ((uint32_t)rloc & 7u)));
                 if constexpr (kFp8) {
-                    const bool row = rtile < u.nrows;
-                    bool range = false;
-                    v[k].x = decode::bf16x2_to_f16x2(v[k].x, range);
-                    v[k].y = decode::bf16x2_to_f16x2(v[k].y, range);
-                    v[k].z = decode::bf16x2_to_f16x2(v[k].z, range);
-                    v[k].w = decode::bf16x2_to_f16x2(v[k].w, range);
-                    q_range |= range && row;
+                    q_to_f16(v[k], rtile < u.nrows);
                 }
             }
         };
@@ -643,17 +648,14 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 for (int j = 0; j < 20; ++j) {
                     const uint32_t at = sbase + kOffQ + 16u * (uint32_t)(qt + 128 * j);
                     uint4 x = ld_shared_v4u(at);
-                    bool range = false;
-                    x.x = decode::bf16x2_to_f16x2(x.x, range);
-                    x.y = decode::bf16x2_to_f16x2(x.y, range);
-                    x.z = decode::bf16x2_to_f16x2(x.z, range);
-                    x.w = decode::bf16x2_to_f16x2(x.w, range);
+                    q_to_f16(x, kCtaRows * (int)rank + (((qt + 128 * j) >> 3) & 63) < u.nrows);
                     st_shared_v4u(at, x.x, x.y, x.z, x.w);
-                    q_range |= range && kCtaRows * (int)rank + (((qt + 128 * j) >> 3) & 63) < u.nrows;
                 }
                 fence_proxy_async_smem();
                 signal_leader(kBarQHiFull, 30 + quarter);
-                if (__any_sync(0xffffffffu, q_range) && lane == 0) raise_error(32 /* MLA_DEVERR_Q_RANGE */);
+                // (0x477F: the largest bf16 below 65504; infinities and NaN lie above, too)
+                const bool range = (q_top & 0xFFFFu) > 0x477Fu || (q_top >> 16) > 0x477Fu;
+                if (__any_sync(0xffffffffu, range) && lane == 0) raise_error(32 /* MLA_DEVERR_Q_RANGE */);
                 __syncwarp();
             }
             // ---- the unit before: its result
