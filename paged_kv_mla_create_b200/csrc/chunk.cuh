@@ -7,11 +7,16 @@
 // A unit is a tile of 128 query rows of one request (row = token * h + head, so one token of 128
 // heads, or eight of 16): the rows share their keys, S = Q K^T and O = P V are dense contractions.
 // One 2-CTA cluster per plan part walks the part's units (chunk_plan.cuh), computing with pair
-// MMAs as the decode kernel does (decode.cuh describes the pair's layout: S split by tokens, O by
-// output columns, the partner's V loaded into the chunks that S no longer needs).  With hundreds of
-// units per part the tensor pipe bounds it (a tile of 128 keys takes ~2,170 cycles of MMAs); with
-// one token per request the cache is read once and HBM does.
+// MMAs in the decode kernel's layout (decode.cuh: S split by tokens, O by output columns, the
+// partner's V loaded into the chunks that S no longer needs).
 //
+//   * 16 warps a CTA, so that every stage has its own: two warps issue S and PV (neither waits
+//     behind the other's barriers), eight run the softmax (32 keys of a row a thread; the two 64-key
+//     halves of four warps took 1.9x as long from S to P), four bring Q and write the result.
+//   * From one unit to the next nothing stands still that need not: the next unit's Q is half in
+//     registers and half in shared memory when the last S MMA releases it (775 cycles from there to Q in
+//     place; 3,500 as row-per-thread loads), its first S and softmax run while the Q warps write the
+//     unit before, from row sums handed over in shared memory.
 //   * A unit that lies whole in its part writes bf16 o and lse.  A part's first unit may continue
 //     one that the part before began, its last may go on in the next: such pieces store fp32
 //     partials in slot 2 part (continued) or 2 part + 1 (begun here), and chunk_merge_kernel joins
@@ -19,6 +24,14 @@
 //     piece waits for another.
 //   * Rows of a page at or past L (never written) are cleared in shared memory before P V reads
 //     them: P is 0 there, but 0 x NaN is not.
+//
+// What bounds it.  A tile of 128 keys is ~2,170 cycles of MMAs; a two-slot page ring turns round in
+// load 900 + S + softmax 2,000 + PV + signals, which leaves ~3,240 cycles a tile (bf16).  At that rate
+// a long chunk runs into the power limit (1.44-1.72 GHz): 2,000 tokens of 128 heads at 32,768 keys take
+// 15.8 ms, 1.19 PFLOP/s, 84 % of a sustained library GEMM.  An 8-bit cache adds the widening to every
+// tile (~3,800 cycles, 0.83 PFLOP/s).  One token a request reads the cache once: 64 requests of ~2,500
+// keys take 70 us, 2.8 TB/s.  Separate rings for K groups and V pieces (V read twice) were slower: 136 KB
+// into the SM per tile instead of 104, at ~57 bytes a cycle.
 #pragma once
 #include "chunk_plan.cuh"
 #include "decode.cuh"
@@ -56,7 +69,7 @@ using decode::PageWindow;
 
 constexpr int kThreads = 512;          // 16 warps: 0 K loads, 1 S issuer, 2 PV issuer (leader), 3 partner V
                                        // (8-bit cache: K of odd tiles), 4..7 and 12..15 softmax, 8..11 Q
-                                       // (8-bit cache: and partner V)
+                                       // and o (8-bit cache: and partner V)
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
 constexpr int kLoBoxes = kQLoChunks;   // a page's chunks 0..3 and 4..8 load, and free their slot, apart

@@ -12,7 +12,8 @@
 //   list), free_pages[off_b + p - have_b] for have_b <= p < cdiv(L_b, 64);
 //   token cu[b] + i: position p_b + i, slot 64 page(b, pos / 64) + pos % 64.
 //
-// Latency bounds it (a few KB to a few MB).  Both prefix sums run over requests only, so every CTA
+// Latency bounds it (a few KB to a few MB; 6.3 us for 64 single tokens, 8.3 us for 96 long chunks
+// with 2 MB of maps, replayed in a graph).  Both prefix sums run over requests only, so every CTA
 // computes them for itself in shared memory, instead of one CTA handing them to the others through
 // a second launch or a grid-wide wait; then CTA 0 plans, and the others fill 1024 entries each of
 // the table and of the token maps (a token finds its request by bisection in shared memory).
@@ -28,7 +29,9 @@ constexpr int kMetaPerThread = 4;        // table or token entries per thread
 constexpr int kMetaPerCta = kMetaThreads * kMetaPerThread;
 constexpr int kTileRows = 128;           // query rows of an attention unit
 constexpr int kTileKeys = 128;           // keys of an attention tile
-// Cost model of the plan, in key tiles: a unit's (query tile's) fixed cost and the shortest piece.
+// Cost model of the plan, in key tiles: a unit's (query tile's) fixed cost and the shortest piece
+// (costs of 1.5 and 2: few heads' prompts 10 % and 3 % slower; of 4: 64 single tokens 4 %; pieces of at
+// least 1, 2 or 4 tiles made no difference).
 constexpr double kUnitCost = 3.0;
 constexpr int kMinPiece = 2;
 
