@@ -430,7 +430,8 @@ MLA_API size_t mla_chunk_workspace_bytes(int32_t num_parts);
  *   A row with no allowed key gets o = 0 and lse = -inf.  Rows of no request (behind the last one)
  *   are left as they were.
  *
- *   q              bf16 [num_tokens, h_q, head_dim], contiguous (e4m3 q: MLA_ERR_UNSUPPORTED)
+ *   q              bf16 [num_tokens, h_q, head_dim], contiguous (e4m3 q: MLA_ERR_UNSUPPORTED); a row
+ *                  that holds NaN gets NaN in o and lse, the other rows nothing of it
  *   head_dim, head_dim_v, k_cache .. max_pages, softmax_scale, descale_q, descale_k  as for
  *                  mla_decode_paged.  Rows of a page at or past L may hold anything (infinities and
  *                  NaN too); the rows below L must be finite

@@ -512,7 +512,8 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             mbar_arrive_expect_tx(bar(kBarQLo), 2 * kBox);
             tma_load_3d(stage, &qlo_map, bar(kBarQLo), 0, v.row0 + kCtaRows * (int)rank, 2 * hb);
         };
-        // bf16 -> f16, keeping the largest magnitude of the unit's rows (past 65504 f16 has no value)
+        // bf16 -> f16, keeping the largest magnitude of the unit's rows (past 65504 f16 has no value;
+        // below it only magnitudes under 2^-17 round, by 2^-25 at most)
         auto q_to_f16 = [&](uint4& x, bool row) {
             uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -560,8 +561,9 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
             const float* x = xmax + kUnitSums + (ue & 1u) * kUnitSumsStride + rloc;
             const float l_run = (x[0] + x[64]) + (x[128] + x[192]);
             const float m_run = x[kSoftmaxThreads];
-            const float inv = l_run > 0.f ? dk / l_run : 0.f;
-            const float lse_val = l_run > 0.f ? (m_run + __log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+            // (0: no key; a NaN goes on into o and lse)
+            const float inv = l_run != 0.f ? dk / l_run : 0.f;
+            const float lse_val = l_run != 0.f ? (m_run + __log2f(l_run)) * 0.69314718055994531f : -INFINITY;
             const bool direct = done.slot < 0;
             const int r0 = kCtaRows * (int)rank + 32 * (quarter & 1);   // the warp's first row
             const int rows = direct ? min(32, done.nrows - r0) : 32;    // rows to write (<= 0: none)
@@ -882,7 +884,8 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 }
                 tc_fence_before();
                 signal_leader(kBarSFree + sb, 18 + sw8);
-                // scale to log2 units, mask the keys at or past the limit, these keys' maximum
+                // scale to log2 units, mask the keys at or past the limit, these keys' maximum (a NaN among
+                // the others, from q, wins it: with the plain maximum the row would look as if it had no key)
                 const int kbase = (u.t0 + i) * kTileKeys + kPage * half + 32 * sub;
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) mul2(s[j], s[j + 1], sl2);
@@ -893,13 +896,13 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 }
                 float hmax;
                 {
-                    float m0 = fmaxf(s[0], s[1]), m1 = fmaxf(s[2], s[3]);
+                    float m0 = max_nan(s[0], s[1]), m1 = max_nan(s[2], s[3]);
 #pragma unroll
                     for (int j = 4; j < 32; j += 4) {
-                        m0 = fmax3(m0, s[j], s[j + 1]);
-                        m1 = fmax3(m1, s[j + 2], s[j + 3]);
+                        m0 = max3_nan(m0, s[j], s[j + 1]);
+                        m1 = max3_nan(m1, s[j + 2], s[j + 3]);
                     }
-                    hmax = fmaxf(m0, m1);
+                    hmax = max_nan(m0, m1);
                 }
                 // three other threads hold the row's other keys
                 xmax[sb * kSoftmaxThreads + 128 * sub + t] = hmax;
@@ -911,10 +914,10 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
                 float tmax;
                 {
                     const float* x = xmax + sb * kSoftmaxThreads + rloc;
-                    tmax = fmaxf(fmaxf(x[0], x[64]), fmaxf(x[128], x[192]));
+                    tmax = max_nan(max_nan(x[0], x[64]), max_nan(x[128], x[192]));
                 }
-                const float m_new = fmaxf(m_run, tmax);
-                const bool rescale = m_new > m_run + kRescaleThreshold;
+                const float m_new = max_nan(m_run, tmax);
+                const bool rescale = m_new > m_run + kRescaleThreshold || m_new != m_new;   // (a NaN, too)
                 float factor = 1.f;
                 if (rescale) {
                     factor = fast_exp2(m_run - m_new);  // 0 when m_run = -inf
@@ -1020,9 +1023,9 @@ __device__ __forceinline__ void merge_unit_row(const int32_t* __restrict__ plan,
         return part_lse[slot_row(k)];
     };
     const float l0 = lse_of(lane);   // of the first 32 pieces, a lane each
-    float mx = l0;
-    for (int k = lane + 32; k < pieces; k += 32) mx = fmaxf(mx, lse_of(k));
-    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    float mx = l0;           // (a NaN piece makes the row NaN)
+    for (int k = lane + 32; k < pieces; k += 32) mx = max_nan(mx, lse_of(k));
+    for (int d = 16; d > 0; d >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, d));
     float sum = 0.f;
     if (mx != -INFINITY) {
         sum = expf(l0 - mx);
@@ -1041,10 +1044,11 @@ __device__ __forceinline__ void merge_unit_row(const int32_t* __restrict__ plan,
             float wt[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                wt[j] = __shfl_sync(0xffffffffu, wl, (k0 + j) & 31);   // 0 past the last piece
+                wt[j] = __shfl_sync(0xffffffffu, wl, (k0 + j) & 31);
+                if (k0 + j >= pieces) wt[j] = 0.f;
 #pragma unroll
                 for (int c = 0; c < kCols / 4; ++c)
-                    v[j][c] = wt[j] > 0.f ? *reinterpret_cast<const float4*>(part_o + slot_row(k0 + j) * kDv + col0 + 128 * c + 4 * lane)
+                    v[j][c] = wt[j] != 0.f ? *reinterpret_cast<const float4*>(part_o + slot_row(k0 + j) * kDv + col0 + 128 * c + 4 * lane)
                                           : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll

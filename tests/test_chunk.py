@@ -555,6 +555,57 @@ def test_two_streams_at_once():
         assert torch.equal(o[:b.tokens], alone[2][:b.tokens]) and torch.equal(lse[:b.tokens], alone[3][:b.tokens])
 
 
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("parts", [1, 74])
+def test_nan_queries_give_nan_in_their_rows_alone(parts, kv):
+    """A row whose query holds NaN gets NaN (o and lse) whether or not the plan cuts its unit; a length below a
+    softmax thread's 32 keys among them.  The other rows keep their bits."""
+    b = Batch([4000, 3, 200], [2, 1, 40], seed=4)
+    h = 64
+    bt, seqlens, cu, _, _, plan, _ = b.maps(h, num_parts=parts)
+    cache, scale, _ = make_cache(b, kv, 5)
+    q = torch.randn(b.rows, h, 576, generator=torch.Generator(device="cuda").manual_seed(6), device="cuda").bfloat16()
+    call = lambda x: mla.mla_chunk_paged(x, cache, bt, seqlens, cu, 512, plan, SCALE, descale_k=scale)
+    o0, lse0 = call(q)
+    assert mla.read_device_error() == 0
+    bad = torch.zeros(b.rows, h, dtype=torch.bool, device="cuda")
+    bad[0, 5] = bad[1, 63] = bad[2, 0] = bad[30, 33] = bad[42, 40] = True
+    nan = q.clone()
+    nan[bad, 100] = float("nan")
+    o, lse = call(nan)
+    assert mla.read_device_error() == (0 if kv == "bf16" else 32)
+    assert bool(lse[bad].isnan().all()) and bool(o[bad].isnan().all())
+    assert torch.equal(o[~bad], o0[~bad]) and torch.equal(lse[~bad], lse0[~bad])
+
+
+@gpu
+def test_query_scale_and_a_strided_table():
+    """descale_q of a power of two undoes q's; a table that is part of a wider one; no rows at all."""
+    b = Batch([300, 70], [5, 40], seed=3)
+    bt, seqlens, cu, _, _, plan, _ = b.maps(16)
+    cache, scale, values = make_cache(b, "e5m2", 1)
+    q = torch.randn(b.rows, 16, 576, device="cuda").bfloat16()
+    o, lse = mla.mla_chunk_paged(q, cache, bt, seqlens, cu, 512, plan, SCALE, descale_k=scale)
+    wide = torch.full((bt.shape[0], bt.shape[1] + 9), -1, dtype=torch.int32, device="cuda")
+    wide[:, 4:4 + bt.shape[1]] = bt
+    half = torch.full((1,), 0.5, device="cuda")
+    o2, lse2 = mla.mla_chunk_paged(2 * q, cache, wide[:, 4:4 + bt.shape[1]], seqlens, cu, 512, plan, SCALE, descale_q=half,
+                                   descale_k=scale)
+    # q becomes f16 here: exact, and so the same bits, but for values below 2^-17, whose bits end below
+    # f16's smallest step, 2^-24.  Those round by at most 2^-25 in q and, halved again, 2^-26 in 2 q, so a
+    # row's scores differ by ds <= SCALE sum_d |k_d| (2^-25 + 2^-26) at most, lse by ds (and fp32's rounding
+    # of it), o by 2 ds sum_j p_j |v_j|, p's two roundings to f16 and its own two to bf16.
+    exact = (2 * q.half() == (2 * q).half()).all(-1)
+    assert torch.equal(o[exact], o2[exact]) and torch.equal(lse[exact], lse2[exact])
+    vmax = float(values.abs().max())
+    ds = SCALE * 576 * vmax * 1.5 * 2.0**-25
+    assert bool(((lse - lse2).abs() <= ds + 2.0**-22 * lse.abs()).all())
+    assert bool(((o.double() - o2.double()).abs() <= (2 * ds + 2 * 2.0**-11) * vmax + 2 * 2.0**-8 * o.double().abs()).all())
+    none, _ = mla.mla_chunk_paged(q[:0], cache, bt, seqlens, cu, 512, plan, SCALE, descale_k=scale)
+    assert none.shape == (0, 16, 512) and mla.read_device_error() == 0
+
+
 # ------------------------------------------------------------------------- errors and refusals
 @gpu
 def test_bad_pages_and_offsets_are_reported_or_clamped():
