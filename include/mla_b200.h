@@ -387,6 +387,9 @@ MLA_API mla_status_t mla_extend_paged_prefix(const void* q, int32_t bs, int32_t 
  * pages from its list.  The requests' rows must differ then (two requests of one row would enter
  * their slots at the same places).
  *
+ * What is written overlaps nothing that is read, but for req_to_token: cache_seqlens at the address
+ * of prefix_lens or chunk_lens is MLA_ERR_INVALID_ARG.
+ *
  *   req_to_token   int32 [req_to_token_rows, req_to_token_stride]
  *   req_pool_indices [bs] and free_pages [num_free_pages] of index_dtype (int32 or int64)
  *   prefix_lens, chunk_lens [bs] of lens_dtype (int32 or int64); negative ones count as 0

@@ -478,6 +478,8 @@ def build_chunk_metadata(req_to_token: torch.Tensor, req_pool_indices: torch.Ten
         raise ValueError("req_to_token must be a row-major int32 matrix")
     if num_tokens < 0 or max_seqlen_pad < 0 or num_heads <= 0:
         raise ValueError("num_tokens and max_seqlen_pad must not be negative, num_heads must be positive")
+    if max(num_tokens, max_seqlen_pad, num_heads, abs(pad_slot), num_parts or 0) > 0x7FFFFFFF:
+        raise ValueError("num_tokens, max_seqlen_pad, num_heads, pad_slot and num_parts must fit into 32 bits")
     bs = req_pool_indices.shape[0]
     if not (tuple(req_pool_indices.shape) == tuple(prefix_lens.shape) == tuple(chunk_lens.shape) == (bs,)):
         raise ValueError("req_pool_indices, prefix_lens and chunk_lens must be vectors of one entry per request")

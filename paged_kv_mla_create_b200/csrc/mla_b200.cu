@@ -629,6 +629,8 @@ mla_status_t mla_build_chunk_metadata(
     if (num_free_pages < 0 || (free_pages && num_free_pages > INT32_MAX)) return MLA_ERR_INVALID_ARG;
     if (!cu_seqlens || !chunk_plan) return MLA_ERR_INVALID_ARG;
     if (!is_aligned(chunk_plan, 16)) return MLA_ERR_INVALID_ARG;
+    // other CTAs read the lengths while the first writes cache_seqlens
+    if (cache_seqlens && (cache_seqlens == prefix_lens || cache_seqlens == chunk_lens)) return MLA_ERR_INVALID_ARG;
     if (bs > 0 && (!req_to_token || !req_pool_indices || !prefix_lens || !chunk_lens || !cache_seqlens ||
                    (max_pages > 0 && !block_table)))
         return MLA_ERR_INVALID_ARG;

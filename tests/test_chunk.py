@@ -695,6 +695,19 @@ def test_binding_refusals():
     assert mla.read_device_error() == 0
 
 
+@gpu
+def test_numbers_past_32_bits_are_refused():
+    b = Batch([30, 0], [5, 7], seed=3)
+    args = dict(req_to_token=b.r2t, req_pool_indices=b.rpi, prefix_lens=b.prefix_t, chunk_lens=b.chunk_t, num_tokens=12,
+                max_seqlen_pad=1, num_heads=16, free_pages=b.free)
+    out = mla.build_chunk_metadata(**args)
+    for kw in (dict(num_tokens=2**32 + 12), dict(max_seqlen_pad=2**32 + 1), dict(num_heads=2**32 + 16), dict(pad_slot=2**31),
+               dict(num_parts=2**32 + 74)):
+        with pytest.raises(ValueError):
+            mla.build_chunk_metadata(**{**args, "out": out, **kw})
+    assert mla.read_device_error() == 0
+
+
 # ----------------------------------------------------------------------------- without a GPU
 def test_chunk_sizes():
     lib = mla.library()
@@ -735,6 +748,8 @@ def test_chunk_metadata_validation_happens_before_any_launch():
                *[{x: None} for x in ("r2t", "rpi", "prefix", "chunk", "bt", "seqlens", "cu", "pos", "loc", "plan")]):
         assert bad(**kw) == 1, kw
     assert bad(bs=4097) == 2 and bad(tokens=1 << 27) == 2
+    # the lengths that are read may not be the ones that are written
+    assert bad(seqlens=1 << 22) == 1 and bad(seqlens=1 << 23) == 1
 
 
 def test_chunk_calls_refuse_cpu_tensors():
