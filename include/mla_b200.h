@@ -1,7 +1,8 @@
 /*
  * mla_b200.h — C ABI of the B200 (sm_100a) paged MLA decode library.
  *
- * Three operations, in the order a decode step calls them, each in the role the
+ * Three operations, in the order a decode step calls them (and, further down, the same for batches
+ * whose requests bring any number of new tokens: mla_build_chunk_metadata, mla_chunk_paged), each in the role the
  * SGLang FlashMLA attention backend page (flashmla_backend.py) gives it:
  *
  *   mla_build_block_table  the per-request page table of

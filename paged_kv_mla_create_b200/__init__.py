@@ -16,6 +16,9 @@ The three entry points follow the calls of the SGLang FlashMLA attention backend
 * ``mla_decode_paged``    — ``flash_mla_with_kvcache(q, k_cache, block_table,
   cache_seqlens, head_dim_v, tile_scheduler_metadata, num_splits, softmax_scale,
   causal, descale_q, descale_k)`` returning (o, lse); also exported under that name.
+
+For requests that bring different numbers of new tokens: ``build_chunk_metadata`` (page table, lengths,
+positions, pool slots and plan from the requests' lengths), ``set_kv_buffer``, ``mla_chunk_paged``.
 """
 from __future__ import annotations
 

@@ -11,11 +11,12 @@
 // partner's V loaded into the chunks that S no longer needs).
 //
 //   * 16 warps a CTA, so that every stage has its own: two warps issue S and PV (neither waits
-//     behind the other's barriers), eight run the softmax (32 keys of a row a thread; the two 64-key
-//     halves of four warps took 1.9x as long from S to P), four bring Q and write the result.
+//     behind the other's barriers), eight run the softmax (32 keys of a row a thread), four bring Q
+//     and write the result.  (Four softmax warps of 64 keys a thread and one issuer: 2,000 tokens at
+//     32,768 keys took 16.7 ms instead of 16.0.)
 //   * From one unit to the next nothing stands still that need not: the next unit's Q is half in
-//     registers and half in shared memory when the last S MMA releases it (775 cycles from there to Q in
-//     place; 3,500 as row-per-thread loads), its first S and softmax run while the Q warps write the
+//     registers and half in shared memory when the last S MMA releases it (traced: 775 cycles from there to
+//     Q in place; 3,500 as row-per-thread loads), its first S and softmax run while the Q warps write the
 //     unit before, from row sums handed over in shared memory.
 //   * A unit that lies whole in its part writes bf16 o and lse.  A part's first unit may continue
 //     one that the part before began, its last may go on in the next: such pieces store fp32
@@ -28,10 +29,10 @@
 // What bounds it.  A tile of 128 keys is ~2,170 cycles of MMAs; a two-slot page ring turns round in
 // load 900 + S + softmax 2,000 + PV + signals, which leaves ~3,240 cycles a tile (bf16).  At that rate
 // a long chunk runs into the power limit (1.44-1.72 GHz): 2,000 tokens of 128 heads at 32,768 keys take
-// 15.8 ms, 1.19 PFLOP/s, 84 % of a sustained library GEMM.  An 8-bit cache adds the widening to every
-// tile (~3,800 cycles, 0.83 PFLOP/s).  One token a request reads the cache once: 64 requests of ~2,500
-// keys take 70 us, 2.8 TB/s.  Separate rings for K groups and V pieces (V read twice) were slower: 136 KB
-// into the SM per tile instead of 104, at ~57 bytes a cycle.
+// 15.8 ms (calls in a row), 1.19 PFLOP/s, 84 % of a sustained library GEMM.  An 8-bit cache adds the
+// widening to every tile (~3,800 cycles, 0.83 PFLOP/s).  One token a request reads the cache once: 64
+// requests of ~2,500 keys take 70 us replayed in a graph, 2.9 TB/s.  Separate rings for K groups and V
+// pieces (V read twice) were slower: 136 KB into the SM per tile instead of 104, at ~57 bytes a cycle.
 #pragma once
 #include "chunk_plan.cuh"
 #include "decode.cuh"
