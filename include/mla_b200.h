@@ -413,6 +413,19 @@ MLA_API mla_status_t mla_build_chunk_metadata(
     int32_t fill_tail, int32_t pad_slot, int32_t* cache_seqlens, int32_t* cu_seqlens, int32_t* positions,
     int32_t* cache_loc, int32_t* chunk_plan, int32_t* pages_taken, mla_stream_t stream);
 
+/*
+ * The same for a req_to_token that is part of a wider matrix: its rows lie req_to_token_stride entries
+ * apart, and req_to_token_cols of each (the stride's at most) are the map's.  Nothing else is read or
+ * written: a position past those columns gets slot -1 and sets MLA_DEVERR_LEN_OUT_OF_RANGE.
+ */
+MLA_API mla_status_t mla_build_chunk_metadata_view(
+    int32_t* req_to_token, int64_t req_to_token_rows, int64_t req_to_token_stride, int64_t req_to_token_cols,
+    const void* req_pool_indices, int32_t index_dtype, const void* prefix_lens, const void* chunk_lens, int32_t lens_dtype,
+    int32_t bs, int32_t num_tokens, const void* free_pages, int64_t num_free_pages, int32_t num_heads, int32_t causal,
+    int32_t num_parts, int32_t* block_table, int64_t block_table_stride, int32_t max_pages, int32_t page_size,
+    int32_t fill_tail, int32_t pad_slot, int32_t* cache_seqlens, int32_t* cu_seqlens, int32_t* positions,
+    int32_t* cache_loc, int32_t* chunk_plan, int32_t* pages_taken, mla_stream_t stream);
+
 /* Parts of a chunk_plan: one per pair of SMs.  Returns -1 on a non-positive argument.  Pure host. */
 MLA_API int32_t mla_num_chunk_parts(int32_t sm_count);
 

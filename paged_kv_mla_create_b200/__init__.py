@@ -99,6 +99,9 @@ def library() -> ctypes.CDLL:
     lib.mla_build_chunk_metadata.argtypes = [P, I64, I64, P, I32, P, P, I32, I32, I32, P, I64, I32, I32, I32, P, I64, I32,
                                              I32, I32, I32, P, P, P, P, P, P, P]
     lib.mla_build_chunk_metadata.restype = I32
+    lib.mla_build_chunk_metadata_view.argtypes = [P, I64, I64, I64, P, I32, P, P, I32, I32, I32, P, I64, I32, I32, I32, P, I64,
+                                                  I32, I32, I32, I32, P, P, P, P, P, P, P]
+    lib.mla_build_chunk_metadata_view.restype = I32
     lib.mla_num_chunk_parts.argtypes = [I32]
     lib.mla_num_chunk_parts.restype = I32
     lib.mla_chunk_workspace_bytes.argtypes = [I32]
@@ -516,12 +519,12 @@ def build_chunk_metadata(req_to_token: torch.Tensor, req_pool_indices: torch.Ten
     # a free list without entries is still a list (its data pointer may be null)
     free_ptr = None if free_pages is None else free_pages.data_ptr() or rpi.data_ptr()
     with _on(dev):
-        _check(library().mla_build_chunk_metadata(
-            _addr(req_to_token), req_to_token.shape[0], req_to_token.stride(0), _addr(rpi), _index_dtype(rpi), _addr(pl),
-            _addr(cl), _index_dtype(pl), bs, int(num_tokens), free_ptr, free_pages.shape[0] if free_pages is not None else 0,
-            int(num_heads), int(bool(causal)), parts, _addr(bt), bt.stride(0), int(max_seqlen_pad), PAGE_SIZE,
-            int(bool(fill_tail)), int(pad_slot), _addr(seqlens), _addr(cu), _addr(positions), _addr(loc), _addr(plan),
-            _addr(taken), _stream(dev)), "mla_build_chunk_metadata")
+        _check(library().mla_build_chunk_metadata_view(
+            _addr(req_to_token), req_to_token.shape[0], req_to_token.stride(0), req_to_token.shape[1], _addr(rpi),
+            _index_dtype(rpi), _addr(pl), _addr(cl), _index_dtype(pl), bs, int(num_tokens), free_ptr,
+            free_pages.shape[0] if free_pages is not None else 0, int(num_heads), int(bool(causal)), parts, _addr(bt),
+            bt.stride(0), int(max_seqlen_pad), PAGE_SIZE, int(bool(fill_tail)), int(pad_slot), _addr(seqlens), _addr(cu),
+            _addr(positions), _addr(loc), _addr(plan), _addr(taken), _stream(dev)), "mla_build_chunk_metadata")
     return out
 
 

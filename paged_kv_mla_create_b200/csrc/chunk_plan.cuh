@@ -38,7 +38,7 @@ constexpr int kMinPiece = 2;
 
 struct MetaParams {
     int32_t* req_to_token;
-    int64_t r2t_rows, r2t_stride;
+    int64_t r2t_rows, r2t_stride, r2t_cols;   // a row's pitch, and the columns of it that are the map's
     const void* rpi;
     const void* prefix_lens;
     const void* chunk_lens;
@@ -88,8 +88,8 @@ __device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b, int32_t cap) {
     return s > cap ? cap : (int32_t)s;
 }
 
-// Lengths of a request, made safe: no negative ones, positions past the table or past the row of
-// req_to_token have no page.
+// Lengths of a request, made safe: no negative ones, positions past the table or past the columns
+// of req_to_token have no page.
 struct Req {
     int64_t row, p, L;
     int32_t have, total;   // pages holding cached tokens, pages holding all tokens
@@ -108,7 +108,7 @@ __device__ __forceinline__ Req load_req(const MetaParams& a, int b) {
     r.n = (int32_t)n;
     r.L = p + n;
     int64_t cap = (int64_t)a.max_pages * 64;
-    if (cap > a.r2t_stride) cap = a.r2t_stride;
+    if (cap > a.r2t_cols) cap = a.r2t_cols;
     r.too_long = r.L > cap;
     const int64_t pc = p < cap ? p : cap, lc = r.L < cap ? r.L : cap;
     r.have = (int32_t)((pc + 63) / 64);
@@ -359,7 +359,7 @@ chunk_metadata_kernel(const __grid_constant__ MetaParams a) {
             const Req r = load_req<IdxT, LenT>(a, b);
             const int64_t pos = r.p + (t - s.cu[b]);
             int32_t slot = -1;
-            if (r.row_ok && pos < (int64_t)r.total * 64 && pos < a.r2t_stride) {
+            if (r.row_ok && pos < (int64_t)r.total * 64 && pos < a.r2t_cols) {
                 int32_t* where = a.req_to_token + r.row * a.r2t_stride + pos;
                 if (a.free_pages) {
                     const int32_t page = page_of<IdxT>(a, r, s.off[b], (int32_t)(pos / 64), err);

@@ -613,9 +613,9 @@ mla_status_t mla_extend_paged_prefix(const void* q, int32_t bs, int32_t e, int32
                            reinterpret_cast<const float*>(at(L.lse2)), (int64_t)rows, 512, out, lse, stream);
 }
 
-mla_status_t mla_build_chunk_metadata(
-    int32_t* req_to_token, int64_t req_to_token_rows, int64_t req_to_token_stride, const void* req_pool_indices,
-    int32_t index_dtype, const void* prefix_lens, const void* chunk_lens, int32_t lens_dtype, int32_t bs,
+mla_status_t mla_build_chunk_metadata_view(
+    int32_t* req_to_token, int64_t req_to_token_rows, int64_t req_to_token_stride, int64_t req_to_token_cols,
+    const void* req_pool_indices, int32_t index_dtype, const void* prefix_lens, const void* chunk_lens, int32_t lens_dtype, int32_t bs,
     int32_t num_tokens, const void* free_pages, int64_t num_free_pages, int32_t num_heads, int32_t causal,
     int32_t num_parts, int32_t* block_table, int64_t block_table_stride, int32_t max_pages, int32_t page_size,
     int32_t fill_tail, int32_t pad_slot, int32_t* cache_seqlens, int32_t* cu_seqlens, int32_t* positions,
@@ -635,13 +635,15 @@ mla_status_t mla_build_chunk_metadata(
                    (max_pages > 0 && !block_table)))
         return MLA_ERR_INVALID_ARG;
     if (num_tokens > 0 && (!positions || !cache_loc)) return MLA_ERR_INVALID_ARG;
-    if (bs > 0 && (req_to_token_rows <= 0 || req_to_token_stride <= 0 || block_table_stride < max_pages))
+    if (bs > 0 && (req_to_token_rows <= 0 || req_to_token_stride <= 0 || req_to_token_cols < 0 ||
+                   block_table_stride < max_pages))
         return MLA_ERR_INVALID_ARG;
     if (bs > kMetaMaxRequests || (int64_t)num_tokens * num_heads > INT32_MAX - 256) return MLA_ERR_UNSUPPORTED;
     MetaParams a;
     a.req_to_token = req_to_token;
     a.r2t_rows = req_to_token_rows;
     a.r2t_stride = req_to_token_stride;
+    a.r2t_cols = std::min(req_to_token_cols, req_to_token_stride);
     a.rpi = req_pool_indices;
     a.prefix_lens = prefix_lens;
     a.chunk_lens = chunk_lens;
@@ -675,6 +677,20 @@ mla_status_t mla_build_chunk_metadata(
     else if (l64) chunk_metadata_kernel<int32_t, int64_t><<<grid, kMetaThreads, 0, st>>>(a);
     else chunk_metadata_kernel<int32_t, int32_t><<<grid, kMetaThreads, 0, st>>>(a);
     return from_cuda(cudaGetLastError());
+}
+
+mla_status_t mla_build_chunk_metadata(
+    int32_t* req_to_token, int64_t req_to_token_rows, int64_t req_to_token_stride, const void* req_pool_indices,
+    int32_t index_dtype, const void* prefix_lens, const void* chunk_lens, int32_t lens_dtype, int32_t bs,
+    int32_t num_tokens, const void* free_pages, int64_t num_free_pages, int32_t num_heads, int32_t causal,
+    int32_t num_parts, int32_t* block_table, int64_t block_table_stride, int32_t max_pages, int32_t page_size,
+    int32_t fill_tail, int32_t pad_slot, int32_t* cache_seqlens, int32_t* cu_seqlens, int32_t* positions,
+    int32_t* cache_loc, int32_t* chunk_plan, int32_t* pages_taken, mla_stream_t stream) {
+    return mla_build_chunk_metadata_view(
+        req_to_token, req_to_token_rows, req_to_token_stride, req_to_token_stride, req_pool_indices, index_dtype,
+        prefix_lens, chunk_lens, lens_dtype, bs, num_tokens, free_pages, num_free_pages, num_heads, causal, num_parts,
+        block_table, block_table_stride, max_pages, page_size, fill_tail, pad_slot, cache_seqlens, cu_seqlens, positions,
+        cache_loc, chunk_plan, pages_taken, stream);
 }
 
 int32_t mla_num_chunk_parts(int32_t sm_count) {
