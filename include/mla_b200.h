@@ -453,7 +453,9 @@ MLA_API size_t mla_chunk_workspace_bytes(int32_t num_parts);
  *                  mla_decode_paged.  Rows of a page at or past L may hold anything (infinities and
  *                  NaN too); the rows below L must be finite
  *   cu_seqlens     int32 [bs + 1], non-decreasing, within [0, num_tokens] (other values are clamped)
- *   chunk_plan, num_parts  from mla_build_chunk_metadata for the same lengths, h_q and causal
+ *   chunk_plan, num_parts  from mla_build_chunk_metadata for the same lengths, h_q and causal.  The plan
+ *                  only divides the work: with other lengths than its own (a cut-off cache) or a table of
+ *                  fewer columns the result is that of the lengths given here, the parts less even
  *   out, lse       bf16 [num_tokens, h_q, 512], fp32 [num_tokens, h_q] (written)
  *   workspace      at least mla_chunk_workspace_bytes(num_parts) bytes, 256-byte aligned; calls that
  *                  overlap on the GPU need one each

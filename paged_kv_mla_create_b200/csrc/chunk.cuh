@@ -161,6 +161,12 @@ __device__ __forceinline__ void request_rows(const int32_t* cu, int b, int num_t
     n = c1 - c0;
 }
 
+// Keys of row tile m of a request that the table has columns for.  The merge kernel goes by it too: what
+// is a piece, and what holds keys, follows from the call's lengths, which need not be the plan's.
+__device__ __forceinline__ int table_keys(int L, int n, int h, int m, int causal, int max_keys) {
+    return min(unit_keys(L, n, h, m, causal), max_keys);
+}
+
 // The units of a part, identical in every role.
 struct UnitIter {
     int b, m, t, b1, m1, t1;
@@ -179,7 +185,7 @@ struct UnitIter {
                 m = t = 0;
                 continue;
             }
-            const int keys = min(unit_keys(L, n, p.h, m, p.causal), p.max_keys);
+            const int keys = table_keys(L, n, p.h, m, p.causal, p.max_keys);
             const int tiles = (keys + kTileKeys - 1) / kTileKeys;
             const int hi = (b == b1 && m == m1) ? min(t1, tiles) : tiles;
             const int lo = t;
@@ -1000,8 +1006,10 @@ mla_chunk_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constan
 // Join the pieces of the units that the plan cut: lse = ln sum_i exp(lse_i), o = sum_i
 // exp(lse_i - lse) o_i, in part order.  Part i begins a cut unit when its end lies inside a unit
 // that it does not itself continue; its piece is slot 2 i + 1, and the parts after it that begin
-// inside the same unit hold the others in slot 2 j.  Every CTA lists the cut units from the plan
-// (before it waits for the attention grid: the plan is older than that grid), then its warps take
+// inside the same unit hold the others in slot 2 j.  A unit whose keys end before its first cut is
+// whole, and a piece behind the last key was never written (lengths below the plan's).  Every CTA lists
+// the cut units from the plan and the lengths (before it waits for the attention grid: they are older
+// than that grid), then its warps take
 // whole rows in turn, 16 columns a lane, two pieces' loads in flight -- or, when the cut units'
 // rows are fewer than the warps (few units of many pieces), quarters of rows, 4 columns a lane and
 // eight pieces in flight.
@@ -1010,16 +1018,17 @@ constexpr int kMergeCtasPerPart = 6;   // three CTAs an SM, all resident at once
 constexpr int kMergeMaxParts = 1024;
 
 template <int kCols, int kAhead>
-__device__ __forceinline__ void merge_unit_row(const int32_t* __restrict__ plan, int2 tk, int row, int col0, int64_t orow,
+__device__ __forceinline__ void merge_unit_row(const int32_t* __restrict__ plan, int2 tk, int tiles, int row, int col0, int64_t orow,
                                                const float* __restrict__ part_o, const float* __restrict__ part_lse,
                                                __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int lane) {
     const int pieces = tk.y + 1;
     auto slot_row = [&](int k) { return (int64_t)(k == 0 ? 2 * tk.x + 1 : 2 * (tk.x + k)) * kTileRows + row; };
     auto lse_of = [&](int k) -> float {
         if (k >= pieces) return -INFINITY;
-        if (k > 0) {   // a part that begins inside the unit but holds none of it
+        if (k > 0) {   // a part that begins inside the unit but holds none of its keys
             const int32_t* e = plan + 8 * (int64_t)(tk.x + k);
-            if (e[0] == e[3] && e[1] == e[4] && e[2] >= e[5]) return -INFINITY;
+            const int end = e[0] == e[3] && e[1] == e[4] ? min(e[5], tiles) : tiles;
+            if (e[2] >= end) return -INFINITY;
         }
         return part_lse[slot_row(k)];
     };
@@ -1071,17 +1080,19 @@ __device__ __forceinline__ void merge_unit_row(const int32_t* __restrict__ plan,
 }
 
 __global__ void __launch_bounds__(kMergeThreads, kMergeCtasPerPart / 2)
-chunk_merge_kernel(const int32_t* __restrict__ plan, const int32_t* __restrict__ cu, int32_t parts, int32_t bs, int32_t h,
-                   int32_t num_tokens, const float* __restrict__ part_o, const float* __restrict__ part_lse,
+chunk_merge_kernel(const int32_t* __restrict__ plan, const int32_t* __restrict__ cu,
+                   const int32_t* __restrict__ cache_seqlens, int32_t parts, int32_t bs, int32_t h, int32_t num_tokens,
+                   int32_t max_keys, int32_t causal, const float* __restrict__ part_o, const float* __restrict__ part_lse,
                    __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
     __shared__ int2 task[kMergeMaxParts];   // part that begins the unit, parts that continue it
+    __shared__ int task_tiles[kMergeMaxParts];   // the unit's key tiles
     __shared__ int ntask;
     const int lane = threadIdx.x & 31;
     if (threadIdx.x < 32) {   // in part order: every CTA must number the units alike
         int count = 0;
         for (int i0 = 0; i0 < parts; i0 += 32) {
             const int i = i0 + lane;
-            int n = 0;
+            int n = 0, tiles = 0;
             if (i < parts) {
                 const int32_t* r = plan + 8 * (int64_t)i;
                 const int b = r[3], m = r[4], t = r[5];
@@ -1089,9 +1100,20 @@ chunk_merge_kernel(const int32_t* __restrict__ plan, const int32_t* __restrict__
                 if (t > 0 && b >= 0 && b < bs && m >= 0 && !continues) {
                     for (const int32_t* e = r + 8; i + 1 + n < parts && e[0] == b && e[1] == m && e[2] > 0; e += 8) ++n;
                 }
+                if (n > 0) {
+                    int c0, rows;
+                    request_rows(cu, b, num_tokens, c0, rows);
+                    if ((int64_t)m * kTileRows < (int64_t)rows * h)
+                        tiles = (table_keys(cache_seqlens[b], rows, h, m, causal, max_keys) + kTileKeys - 1) / kTileKeys;
+                    if (t >= tiles) n = 0;   // whole, or no unit at all
+                }
             }
             const unsigned found = __ballot_sync(0xffffffffu, n > 0);
-            if (n > 0) task[count + __popc(found & ((1u << lane) - 1u))] = make_int2(i, n);
+            if (n > 0) {
+                const int at = count + __popc(found & ((1u << lane) - 1u));
+                task[at] = make_int2(i, n);
+                task_tiles[at] = tiles;
+            }
             count += __popc(found);
         }
         if (lane == 0) ntask = count;
@@ -1106,6 +1128,7 @@ chunk_merge_kernel(const int32_t* __restrict__ plan, const int32_t* __restrict__
         const int64_t unit_row = quarters ? w >> 2 : w;
         const int row = (int)(unit_row % kTileRows);
         const int2 tk = task[unit_row / kTileRows];
+        const int tiles = task_tiles[unit_row / kTileRows];
         const int32_t* r = plan + 8 * (int64_t)tk.x;
         int c0, n;
         request_rows(cu, r[3], num_tokens, c0, n);
@@ -1113,9 +1136,9 @@ chunk_merge_kernel(const int32_t* __restrict__ plan, const int32_t* __restrict__
         if (in_req >= (int64_t)n * h) continue;
         const int64_t orow = (int64_t)c0 * h + in_req;
         if (quarters)
-            merge_unit_row<4, 8>(plan, tk, row, 128 * (int)(w & 3), orow, part_o, part_lse, out, lse, lane);
+            merge_unit_row<4, 8>(plan, tk, tiles, row, 128 * (int)(w & 3), orow, part_o, part_lse, out, lse, lane);
         else
-            merge_unit_row<16, 2>(plan, tk, row, 0, orow, part_o, part_lse, out, lse, lane);
+            merge_unit_row<16, 2>(plan, tk, tiles, row, 0, orow, part_o, part_lse, out, lse, lane);
     }
 }
 

@@ -812,8 +812,8 @@ mla_status_t mla_chunk_paged(const void* q, int32_t q_dtype, int32_t num_tokens,
     cfg.gridDim = dim3(kMergeCtasPerPart * num_parts);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    return from_cuda(cudaLaunchKernelEx(&cfg, chunk_merge_kernel, chunk_plan, cu_seqlens, num_parts, bs, h_q, num_tokens,
-                                        (const float*)part_o, (const float*)part_lse, p.out, lse));
+    return from_cuda(cudaLaunchKernelEx(&cfg, chunk_merge_kernel, chunk_plan, cu_seqlens, cache_seqlens, num_parts, bs, h_q,
+                                        num_tokens, p.max_keys, causal, (const float*)part_o, (const float*)part_lse, p.out, lse));
 }
 
 mla_status_t mla_set_test_hooks(uint64_t wait_budget_ns, int32_t withhold_tile, int32_t no_fold_in) {

@@ -1,9 +1,10 @@
-"""Ragged chunks at the edges of what their calls allow: maps that are part of a wider matrix."""
+"""Ragged chunks at the edges of what their calls allow: maps that are part of a wider matrix, lengths other than the
+plan's."""
 import pytest
 import torch
 
 import paged_kv_mla_create_b200 as mla
-from test_chunk import Batch, gpu
+from test_chunk import SCALE, Batch, assert_attention, gpu, make_cache, reference
 
 
 def as_columns(batch, first, cols, behind):
@@ -58,6 +59,38 @@ def test_positions_past_a_views_columns_have_no_slot(cols, given):
                 before[int(b.rpi[r]), 256 + p] = slot
         at += b.chunk[r]
     assert torch.equal(big, before)
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("cut,width", [
+    ([500, 9030, 103], None), ([0, 20, 1], None), ([129, 640, 0], None), ([39000, 8000, 103], None), ([40001, 9040, 103], 5),
+    ([384, 385, 64], 9),
+])
+def test_lengths_below_those_of_the_plan(cut, width, causal, kv):
+    """A plan that cuts long requests over many parts, used with shorter lengths or a narrower table: cuts past a
+    unit's last key leave nothing to merge.  The workspace is NaN: a piece that this call did not write shows."""
+    b = Batch([40000, 9000, 100], [1, 40, 3], seed=3)
+    h = 128
+    bt, _, cu, _, _, plan, _ = b.maps(h, causal=causal)
+    cache, scale, values = make_cache(b, kv, 5)
+    q = torch.randn(b.rows, h, 576, generator=torch.Generator(device="cuda").manual_seed(6), device="cuda").bfloat16()
+    ws = torch.full((mla.chunk_workspace_bytes(mla.num_chunk_parts()),), 255, dtype=torch.uint8, device="cuda")
+    lens = torch.tensor(cut, dtype=torch.int32, device="cuda")
+    table = bt if width is None else bt[:, :width]
+    o, lse = mla.mla_chunk_paged(q, cache, table, lens, cu, 512, plan, SCALE, causal, descale_k=scale, workspace=ws)
+    assert mla.read_device_error() == 0
+    at = 0
+    for r, n in enumerate(b.chunk):
+        L = cut[r]
+        cap = L if width is None else min(L, 64 * width)
+        keys = values[torch.tensor(b.slots[r][:cap], device="cuda", dtype=torch.long)]
+        for i in range(n):   # a token at a time: its limit may lie past the table
+            lim = max(0, min(cap, L - n + i + 1 if causal else L))
+            ro, rl, pv, ds = reference(q[at + i:at + i + 1], keys[:lim], False)
+            assert_attention(o[at + i:at + i + 1], lse[at + i:at + i + 1], ro, rl, pv, ds, lim, kv, float(values.abs().max()))
+        at += n
 
 
 def test_view_validation_happens_before_any_launch():
