@@ -394,7 +394,9 @@ MLA_API mla_status_t mla_extend_paged_prefix(const void* q, int32_t bs, int32_t 
  *   req_to_token   int32 [req_to_token_rows, req_to_token_stride]
  *   req_pool_indices [bs] and free_pages [num_free_pages] of index_dtype (int32 or int64)
  *   prefix_lens, chunk_lens [bs] of lens_dtype (int32 or int64); negative ones count as 0
- *   num_tokens     rows of the batch: at least cu[bs] (what goes beyond is cut off and reported)
+ *   num_tokens     rows of the batch: at least sum_b n_b.  What goes beyond is cut off and reported
+ *                  (MLA_DEVERR_LEN_OUT_OF_RANGE): n_b, and with it L_b, the table, the pages taken and
+ *                  the plan, then count the tokens that have a row
  *   num_parts      mla_num_chunk_parts(sm_count); at most 1024
  *   page_size      must be 64
  * bs at most 4096 and num_tokens * num_heads below 2^31 - 256, else MLA_ERR_UNSUPPORTED.  bs == 0

@@ -88,8 +88,11 @@ __device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b, int32_t cap) {
     return s > cap ? cap : (int32_t)s;
 }
 
-// Lengths of a request, made safe: no negative ones, positions past the table or past the columns
-// of req_to_token have no page.
+// A length, made safe: not negative, in 32 bits.
+__device__ __forceinline__ int64_t safe_len(int64_t x) { return x < 0 ? 0 : (x > INT32_MAX ? INT32_MAX : x); }
+
+// Lengths of a request that brings n tokens, made safe: no negative ones, positions past the table or
+// past the columns of req_to_token have no page.
 struct Req {
     int64_t row, p, L;
     int32_t have, total;   // pages holding cached tokens, pages holding all tokens
@@ -98,14 +101,12 @@ struct Req {
 };
 
 template <typename IdxT, typename LenT>
-__device__ __forceinline__ Req load_req(const MetaParams& a, int b) {
+__device__ __forceinline__ Req make_req(const MetaParams& a, int b, int32_t n) {
     Req r;
     r.row = load_index<IdxT>(a.rpi, b);
-    int64_t p = load_index<LenT>(a.prefix_lens, b), n = load_index<LenT>(a.chunk_lens, b);
-    p = p < 0 ? 0 : (p > INT32_MAX ? INT32_MAX : p);
-    n = n < 0 ? 0 : (n > INT32_MAX ? INT32_MAX : n);
+    const int64_t p = safe_len(load_index<LenT>(a.prefix_lens, b));
     r.p = p;
-    r.n = (int32_t)n;
+    r.n = n;
     r.L = p + n;
     int64_t cap = (int64_t)a.max_pages * 64;
     if (cap > a.r2t_cols) cap = a.r2t_cols;
@@ -117,29 +118,36 @@ __device__ __forceinline__ Req load_req(const MetaParams& a, int b) {
     return r;
 }
 
-// Both prefix sums, saturating (at num_tokens rows, INT32_MAX pages), by the whole CTA.
+// A request as it is after the sums: with the new tokens that have a row (all of them, where num_tokens
+// holds the batch).
 template <typename IdxT, typename LenT>
-__device__ __forceinline__ void scan_requests(const MetaParams& a, MetaSmem& s) {
+__device__ __forceinline__ Req load_req(const MetaParams& a, const MetaSmem& s, int b) {
+    return make_req<IdxT, LenT>(a, b, s.cu[b + 1] - s.cu[b]);
+}
+
+template <typename IdxT, typename LenT>
+__device__ __forceinline__ int32_t new_pages(const MetaParams& a, int b, int32_t n) {
+    const Req r = make_req<IdxT, LenT>(a, b, n);
+    return r.row_ok ? r.total - r.have : 0;
+}
+
+// Turn cu[b + 1] and off[b + 1] (of request b alone) into sums, saturating at `rows` rows and INT32_MAX
+// pages, by the whole CTA.
+__device__ __forceinline__ void sum_requests(int bs, int32_t rows, MetaSmem& s) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (a.bs + kMetaThreads - 1) / kMetaThreads;
-    for (int b = tid; b < a.bs; b += kMetaThreads) {
-        const Req r = load_req<IdxT, LenT>(a, b);
-        s.cu[b + 1] = r.n;
-        s.off[b + 1] = r.row_ok ? r.total - r.have : 0;
-    }
-    if (tid == 0) s.cu[0] = s.off[0] = 0;
+    const int per = (bs + kMetaThreads - 1) / kMetaThreads;
     __syncthreads();
-    const int lo = min(tid * per, a.bs), hi = min(lo + per, a.bs);
+    const int lo = min(tid * per, bs), hi = min(lo + per, bs);
     int32_t n = 0, q = 0;
     for (int b = lo; b < hi; ++b) {
-        n = sat_add(n, s.cu[b + 1], a.num_tokens);
+        n = sat_add(n, s.cu[b + 1], rows);
         q = sat_add(q, s.off[b + 1], INT32_MAX);
     }
     int32_t ni = n, qi = q;
     for (int d = 1; d < 32; d <<= 1) {
         const int32_t tn = __shfl_up_sync(0xffffffffu, ni, d), tq = __shfl_up_sync(0xffffffffu, qi, d);
         if (lane >= d) {
-            ni = sat_add(ni, tn, a.num_tokens);
+            ni = sat_add(ni, tn, rows);
             qi = sat_add(qi, tq, INT32_MAX);
         }
     }
@@ -150,21 +158,45 @@ __device__ __forceinline__ void scan_requests(const MetaParams& a, MetaSmem& s) 
     __syncthreads();
     int32_t bn = 0, bq = 0;   // of the warps and lanes before this thread
     for (int w = 0; w < warp; ++w) {
-        bn = sat_add(bn, s.warp_n[w], a.num_tokens);
+        bn = sat_add(bn, s.warp_n[w], rows);
         bq = sat_add(bq, s.warp_p[w], INT32_MAX);
     }
     const int32_t en = __shfl_up_sync(0xffffffffu, ni, 1), eq = __shfl_up_sync(0xffffffffu, qi, 1);
     if (lane > 0) {
-        bn = sat_add(bn, en, a.num_tokens);
+        bn = sat_add(bn, en, rows);
         bq = sat_add(bq, eq, INT32_MAX);
     }
     for (int b = lo; b < hi; ++b) {
-        bn = sat_add(bn, s.cu[b + 1], a.num_tokens);
+        bn = sat_add(bn, s.cu[b + 1], rows);
         bq = sat_add(bq, s.off[b + 1], INT32_MAX);
         s.cu[b + 1] = bn;
         s.off[b + 1] = bq;
     }
     __syncthreads();
+}
+
+// Both prefix sums, by the whole CTA.  Where the batch has more new tokens than rows, what goes beyond
+// counts nowhere: the lengths, the pages and the plan are those of the tokens that have a row.
+template <typename IdxT, typename LenT>
+__device__ __forceinline__ void scan_requests(const MetaParams& a, MetaSmem& s) {
+    const int tid = threadIdx.x;
+    for (int b = tid; b < a.bs; b += kMetaThreads) {
+        const int32_t n = (int32_t)safe_len(load_index<LenT>(a.chunk_lens, b));
+        s.cu[b + 1] = n;
+        s.off[b + 1] = new_pages<IdxT, LenT>(a, b, n);
+    }
+    if (tid == 0) s.cu[0] = s.off[0] = 0;
+    sum_requests(a.bs, a.num_tokens + 1, s);   // (num_tokens < 2^31 - 256)
+    if (s.cu[a.bs] <= a.num_tokens) return;
+    for (int b = tid; b < a.bs; b += kMetaThreads)
+        s.off[b + 1] = min(s.cu[b + 1], a.num_tokens) - min(s.cu[b], a.num_tokens);
+    __syncthreads();
+    for (int b = tid; b < a.bs; b += kMetaThreads) {
+        const int32_t n = s.off[b + 1];
+        s.cu[b + 1] = n;
+        s.off[b + 1] = new_pages<IdxT, LenT>(a, b, n);
+    }
+    sum_requests(a.bs, a.num_tokens, s);
 }
 
 // Page of entry (b, p), p < total: from the free list or from req_to_token; -1 where there is none.
@@ -198,8 +230,8 @@ __device__ __forceinline__ void plan_chunks(const MetaParams& a, MetaSmem& s) {
     const int h = a.num_heads;
     const double inv_h = 1.0 / h;
     auto len_of = [&](int b, int& n, int& L) {
-        n = s.cu[b + 1] - s.cu[b];
-        const Req r = load_req<IdxT, LenT>(a, b);
+        const Req r = load_req<IdxT, LenT>(a, s, b);
+        n = r.n;
         const int64_t cap = (int64_t)a.max_pages * 64;
         L = (int)(r.L > INT32_MAX ? INT32_MAX : r.L);
         return cap;
@@ -305,11 +337,11 @@ chunk_metadata_kernel(const __grid_constant__ MetaParams a) {
         for (int b = threadIdx.x; b <= a.bs; b += kMetaThreads) {
             a.cu_seqlens[b] = s.cu[b];
             if (b == a.bs) break;
-            const Req r = load_req<IdxT, LenT>(a, b);
+            const Req r = load_req<IdxT, LenT>(a, s, b);
             a.cache_seqlens[b] = (int32_t)(r.L > INT32_MAX ? INT32_MAX : r.L);
             if (!r.row_ok) err |= 2 /* MLA_DEVERR_ROW_OUT_OF_RANGE */;
             if (r.too_long) err |= 4 /* MLA_DEVERR_LEN_OUT_OF_RANGE */;
-            if (r.n > s.cu[b + 1] - s.cu[b]) err |= 4;   // more rows than num_tokens
+            if (safe_len(load_index<LenT>(a.chunk_lens, b)) > r.n) err |= 4;   // more rows than num_tokens
         }
         if (threadIdx.x == 0 && a.pages_taken) {
             const int64_t taken = s.off[a.bs];
@@ -329,7 +361,7 @@ chunk_metadata_kernel(const __grid_constant__ MetaParams a) {
             if (idx >= entries) break;
             const int b = (int)(idx / a.max_pages);
             const int32_t p = (int32_t)(idx - (int64_t)b * a.max_pages);
-            const Req r = load_req<IdxT, LenT>(a, b);
+            const Req r = load_req<IdxT, LenT>(a, s, b);
             int32_t* dst = a.block_table + b * a.bt_stride + p;
             if (r.row_ok && p < r.total)
                 *dst = page_of<IdxT>(a, r, s.off[b], p, err);
@@ -356,7 +388,7 @@ chunk_metadata_kernel(const __grid_constant__ MetaParams a) {
                 if (s.cu[mid] <= t) lo = mid; else hi = mid;
             }
             const int b = lo;
-            const Req r = load_req<IdxT, LenT>(a, b);
+            const Req r = load_req<IdxT, LenT>(a, s, b);
             const int64_t pos = r.p + (t - s.cu[b]);
             int32_t slot = -1;
             if (r.row_ok && pos < (int64_t)r.total * 64 && pos < a.r2t_cols) {

@@ -1,5 +1,5 @@
 """Ragged chunks at the edges of what their calls allow: maps that are part of a wider matrix, lengths other than the
-plan's."""
+plan's, more new tokens than rows."""
 import pytest
 import torch
 
@@ -90,6 +90,58 @@ def test_lengths_below_those_of_the_plan(cut, width, causal, kv):
             lim = max(0, min(cap, L - n + i + 1 if causal else L))
             ro, rl, pv, ds = reference(q[at + i:at + i + 1], keys[:lim], False)
             assert_attention(o[at + i:at + i + 1], lse[at + i:at + i + 1], ro, rl, pv, ds, lim, kv, float(values.abs().max()))
+        at += n
+
+
+@gpu
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("rows", [0, 3, 20, 62, 63, 64, 150, 254])
+def test_tokens_past_the_batchs_rows_do_not_count(rows, given):
+    """More new tokens than rows: reported, and the maps, lengths and pages are those of the tokens that have one."""
+    b = Batch([10, 100, 64, 0], [3, 60, 1, 191], seed=5, given=given)
+    whole = b.chunk
+    b.rows = rows
+    bt, seqlens, cu, pos, loc, plan, taken = out = b.maps()
+    assert mla.read_device_error() == 4
+    kept, left = [], rows
+    for n in whole:
+        kept.append(min(n, left))
+        left -= kept[-1]
+    L = [p + n for p, n in zip(b.prefix, kept)]
+    assert seqlens.tolist() == L and cu.tolist() == [sum(kept[:i]) for i in range(5)]
+    total = [-(-x // 64) for x in L]
+    assert bt.tolist() == [[b.slots[r][64 * p] // 64 for p in range(total[r])] + [-1] * (b.width - total[r]) for r in range(4)]
+    assert loc.tolist() == [s for r in range(4) for s in b.slots[r][b.prefix[r]:L[r]]]
+    assert pos.tolist() == [p for r in range(4) for p in range(b.prefix[r], L[r])]
+    assert given or int(taken) == sum(t - -(-p // 64) for t, p in zip(total, b.prefix))
+    for r in range(4):
+        row = b.r2t[int(b.rpi[r])].tolist()
+        assert row[:L[r]] == b.slots[r][:L[r]] and (given or set(row[L[r]:]) <= {-7})
+    if rows == 0:
+        assert bool((plan == torch.tensor([4, 0, 0, 4, 0, 0, 0, 0], device="cuda")).all())
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_attention_of_a_batch_whose_tokens_were_cut_off(kv):
+    """The rows that are there see the keys up to their own; rows of the dropped tokens hold NaN."""
+    b = Batch([3000, 500, 64], [40, 300, 9], seed=6)
+    h, rows = 64, 200
+    b.rows = rows
+    bt, seqlens, cu, _, _, plan, _ = b.maps(h)
+    assert mla.read_device_error() == 4
+    kept = [40, 160, 0]
+    b.slots = [s[:p + n] for s, p, n in zip(b.slots, b.prefix, kept)]   # the others are no request's: NaN
+    cache, scale, values = make_cache(b, kv, 7)
+    q = torch.randn(rows, h, 576, generator=torch.Generator(device="cuda").manual_seed(8), device="cuda").bfloat16()
+    o, lse = mla.mla_chunk_paged(q, cache, bt, seqlens, cu, 512, plan, SCALE, descale_k=scale)
+    assert mla.read_device_error() == 0
+    at = 0
+    for r, n in enumerate(kept):
+        if n:
+            keys = values[torch.tensor(b.slots[r], device="cuda")]
+            ro, rl, pv, ds = reference(q[at:at + n], keys, True)
+            assert_attention(o[at:at + n], lse[at:at + n], ro, rl, pv, ds, keys.shape[0], kv, float(keys.abs().max()))
         at += n
 
 
