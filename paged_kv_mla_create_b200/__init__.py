@@ -475,7 +475,10 @@ def build_chunk_metadata(req_to_token: torch.Tensor, req_pool_indices: torch.Ten
     Without free_pages the new tokens' slots are read from req_to_token; with them new pages are
     taken from the list, in request order, and the new slots entered into req_to_token (the
     requests' rows must differ then).  Rows behind the last request get position 0 and slot
-    pad_slot when fill_tail (-1: not a slot; set_kv_buffer skips and reports it), else nothing."""
+    pad_slot when fill_tail (-1: not a slot; set_kv_buffer skips and reports it), else nothing.
+
+    out: the tensors to write, in the order of the result; all but the plan, whose rows are the parts',
+    may be larger."""
     if not req_to_token.is_cuda:
         raise ValueError("paged_kv_mla_create_b200 runs on CUDA tensors only")
     dev = req_to_token.device
@@ -513,6 +516,8 @@ def build_chunk_metadata(req_to_token: torch.Tensor, req_pool_indices: torch.Ten
         _int32_vector(positions, "positions", num_tokens)
         _int32_vector(loc, "cache_loc", num_tokens)
         _int32_vector(plan, "chunk_plan", 8 * parts)
+        if plan.numel() != 8 * parts:   # the attention would run rows behind the last as parts
+            raise ValueError(f"chunk_plan must have a row for each of the {parts} parts and no other")
         if taken is not None:
             _int32_vector(taken, "pages_taken", 1)
     bt, taken = out[0], out[6]

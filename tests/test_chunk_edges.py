@@ -1,5 +1,5 @@
 """Ragged chunks at the edges of what their calls allow: maps that are part of a wider matrix, lengths other than the
-plan's, more new tokens than rows."""
+plan's, more new tokens than rows, buffers that do not fit."""
 import pytest
 import torch
 
@@ -143,6 +143,21 @@ def test_attention_of_a_batch_whose_tokens_were_cut_off(kv):
             ro, rl, pv, ds = reference(q[at:at + n], keys, True)
             assert_attention(o[at:at + n], lse[at:at + n], ro, rl, pv, ds, keys.shape[0], kv, float(keys.abs().max()))
         at += n
+
+
+@gpu
+def test_a_plan_buffer_of_other_rows_is_refused():
+    """A plan has a row for each part: rows behind the last would be run as parts by the attention."""
+    b = Batch([30, 0], [5, 7], seed=3)
+    parts = mla.num_chunk_parts()
+    out = list(b.maps())
+    for rows, kw in ((parts + 1, {}), (100, {}), (parts - 1, {}), (parts, dict(num_parts=3)), (3, {})):
+        out[5] = torch.zeros(rows, 8, dtype=torch.int32, device="cuda")
+        with pytest.raises(ValueError, match="chunk_plan"):
+            b.maps(out=tuple(out), **kw)
+    out[5] = torch.zeros(3, 8, dtype=torch.int32, device="cuda")
+    assert b.maps(out=tuple(out), num_parts=3)[5] is out[5]
+    assert mla.read_device_error() == 0
 
 
 def test_view_validation_happens_before_any_launch():
