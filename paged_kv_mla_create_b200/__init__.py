@@ -122,10 +122,18 @@ def _check(status: int, what: str):
         raise MlaError(status, what)
 
 
+# The address of a device's current stream without a Stream object (a private name, as torch's own
+# generated code uses it; without it the public call does the same a few microseconds slower).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _stream(device) -> ctypes.c_void_p:
-    """The device's current stream (device: a torch.device or an index), without a Stream object."""
+    """The device's current stream (device: a torch.device, its name or an index)."""
+    if isinstance(device, str):
+        device = torch.device(device)
     index = device if isinstance(device, int) else device.index
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index))
+    return ctypes.c_void_p(_raw_stream(torch.cuda.current_device() if index is None else index))
 
 
 def _ptr(t: Optional[torch.Tensor]):

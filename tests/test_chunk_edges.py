@@ -1,5 +1,9 @@
 """Ragged chunks at the edges of what their calls allow: maps that are part of a wider matrix, lengths other than the
 plan's, more new tokens than rows, buffers that do not fit."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -166,3 +170,24 @@ def test_view_validation_happens_before_any_launch():
             1 << 27, 1 << 28, 1 << 29, None, None]
     for at, value in ((1, 0), (2, 0), (3, -1), (4, None), (14, 2), (17, 2)):
         assert f(*args[:at], value, *args[at + 1:]) == 1, at
+
+
+@gpu
+def test_a_device_by_any_of_its_names():
+    for device in (None, 0, "cuda", "cuda:0", torch.device("cuda"), torch.device("cuda", 0)):
+        assert mla.read_device_error(device) == 0
+
+
+def test_the_current_stream_is_found_by_any_name_of_the_device(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(mla, "_raw_stream", lambda index: 1000 + index)
+    for device, index in ((0, 0), (2, 2), ("cuda:1", 1), ("cuda", 3), (torch.device("cuda"), 3), (torch.device("cuda", 2), 2)):
+        assert mla._stream(device).value == 1000 + index
+
+
+def test_the_current_stream_without_the_private_call():
+    """A torch without the private name: the public call takes its place."""
+    code = ("import types, torch; torch._C.__dict__.pop('_cuda_getCurrentRawStream', None)\n"
+            "torch.cuda.current_stream = lambda index: types.SimpleNamespace(cuda_stream=500 + index)\n"
+            "import paged_kv_mla_create_b200 as mla; assert mla._stream(7).value == 507")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
