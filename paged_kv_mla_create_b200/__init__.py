@@ -177,7 +177,7 @@ def _index_dtype(t: torch.Tensor) -> int:
 
 
 def sm_count(device=None) -> int:
-    return torch.cuda.get_device_properties(device or torch.cuda.current_device()).multi_processor_count
+    return torch.cuda.get_device_properties(torch.cuda.current_device() if device is None else device).multi_processor_count
 
 
 def num_sm_parts(num_heads_per_head_k: int, num_heads_k: int = 1,
@@ -610,7 +610,7 @@ def read_device_error(device=None) -> int:
     """Synchronise the current stream and return (and clear) the sticky device error word."""
     code = ctypes.c_int32(0)
     status = library().mla_read_device_error(ctypes.byref(code),
-                                             _stream(device or torch.cuda.current_device()))
+                                             _stream(torch.cuda.current_device() if device is None else device))
     if status not in (0, 4):
         raise MlaError(status, "mla_read_device_error")
     return int(code.value)

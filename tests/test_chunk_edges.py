@@ -3,6 +3,7 @@ plan's, more new tokens than rows, buffers that do not fit."""
 import os
 import subprocess
 import sys
+import types
 
 import pytest
 import torch
@@ -191,3 +192,14 @@ def test_the_current_stream_without_the_private_call():
             "torch.cuda.current_stream = lambda index: types.SimpleNamespace(cuda_stream=500 + index)\n"
             "import paged_kv_mla_create_b200 as mla; assert mla._stream(7).value == 507")
     subprocess.run([sys.executable, "-c", code], check=True, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+
+def test_device_zero_is_not_the_current_device(monkeypatch):
+    asked = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "get_device_properties",
+                        lambda d: asked.append(d) or types.SimpleNamespace(multi_processor_count=148 if d == 0 else 20))
+    mla._device_parts.cache_clear()
+    assert mla._device_parts(0) == 74 and mla._device_parts(3) == 10 and mla.sm_count() == 20
+    assert asked == [0, 3, 3]
+    mla._device_parts.cache_clear()
