@@ -196,6 +196,14 @@ def workspace_bytes(bs: int, q_len: int, h_q: int, parts: int) -> int:
     return int(library().mla_decode_workspace_bytes(bs, q_len, h_q, parts))
 
 
+def _map_pages(req_to_token: torch.Tensor, max_pages: int) -> int:
+    """Pages a row of req_to_token has slots for, at most max_pages.  The library takes the row pitch for the
+    width; where the map is part of a wider matrix, the columns that are not its own are never asked for."""
+    if req_to_token.shape[1] >= req_to_token.stride(0):
+        return max_pages
+    return min(max_pages, -(-req_to_token.shape[1] // PAGE_SIZE))
+
+
 def build_block_table(req_to_token: torch.Tensor, req_pool_indices: torch.Tensor,
                       seq_lens: torch.Tensor, max_seqlen_pad: int, seq_len_add: int = 0,
                       out: Optional[torch.Tensor] = None, fill_tail: bool = True) -> torch.Tensor:
@@ -211,10 +219,13 @@ def build_block_table(req_to_token: torch.Tensor, req_pool_indices: torch.Tensor
         raise ValueError("out must be a row-major int32 matrix")
     rpi = req_pool_indices.contiguous()
     sl = seq_lens.contiguous()
+    pages = _map_pages(req_to_token, int(max_seqlen_pad))
+    if fill_tail and pages < max_seqlen_pad:
+        out[:bs, pages:max_seqlen_pad] = -1
     _check(library().mla_build_block_table(
         _ptr(req_to_token), req_to_token.shape[0], req_to_token.stride(0), _ptr(rpi),
         _index_dtype(rpi), _ptr(sl), _index_dtype(sl), int(seq_len_add), bs, _ptr(out),
-        out.stride(0), int(max_seqlen_pad), PAGE_SIZE, int(bool(fill_tail)),
+        out.stride(0), pages, PAGE_SIZE, int(bool(fill_tail)),
         _stream(req_to_token.device)), "mla_build_block_table")
     return out
 
@@ -289,10 +300,13 @@ def build_decode_metadata(req_to_token: torch.Tensor, req_pool_indices: torch.Te
         raise ValueError("out tensors do not match the metadata's shapes")
     rpi = req_pool_indices.contiguous()
     sl = seq_lens.contiguous()
+    pages = _map_pages(req_to_token, int(max_seqlen_pad))
+    if fill_tail and pages < max_seqlen_pad:
+        bt[:bs, pages:max_seqlen_pad] = -1
     _check(library().mla_build_decode_metadata(
         _ptr(req_to_token), req_to_token.shape[0], req_to_token.stride(0), _ptr(rpi),
         _index_dtype(rpi), _ptr(sl), _index_dtype(sl), int(seq_len_add), bs, _ptr(bt), bt.stride(0),
-        int(max_seqlen_pad), PAGE_SIZE, int(bool(fill_tail)), int(num_heads_per_head_k),
+        pages, PAGE_SIZE, int(bool(fill_tail)), int(num_heads_per_head_k),
         int(num_heads_k), int(bool(is_fp8_kvcache)), sms, _ptr(cl), _ptr(md), _ptr(ns),
         _stream(dev)), "mla_build_decode_metadata")
     return bt, cl, md, ns
@@ -435,14 +449,15 @@ def extend_paged_prefix(q: torch.Tensor, k_new: torch.Tensor, k_cache: torch.Ten
         out = torch.empty((bs, e, h_q, 512), dtype=torch.bfloat16, device=dev)
     if lse is None:
         lse = torch.empty((bs, e, h_q), dtype=torch.float32, device=dev)
-    need = extend_workspace_bytes(bs, e, h_q, int(max_prefix_pages)) if bs else 0
+    pages = _map_pages(req_to_token, int(max_prefix_pages))
+    need = extend_workspace_bytes(bs, e, h_q, pages) if bs else 0
     if workspace is None and need:
         workspace = torch.zeros((need,), dtype=torch.uint8, device=dev)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(library().mla_extend_paged_prefix(
         _ptr(q), bs, e, h_q, _ptr(k_new), _ptr(k_cache), _CACHE_DTYPES[k_cache.dtype],
         k_cache.numel() // (PAGE_SIZE * 576), _ptr(req_to_token), int(req_to_token.shape[0]),
-        req_to_token.stride(0), _ptr(rpi), _index_dtype(rpi), _ptr(pl), int(max_prefix_pages),
+        req_to_token.stride(0), _ptr(rpi), _index_dtype(rpi), _ptr(pl), pages,
         float(softmax_scale), _ptr(descale_k), sm_count(dev), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
         _stream(dev)), "mla_extend_paged_prefix")
     return out, lse

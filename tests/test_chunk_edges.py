@@ -67,6 +67,36 @@ def test_positions_past_a_views_columns_have_no_slot(cols, given):
 
 
 @gpu
+@pytest.mark.parametrize("cols", [512, 540])
+def test_table_builders_read_a_views_own_columns_alone(cols):
+    """The decode calls' tables of a map that is part of a wider matrix: a length past its columns is reported and
+    cut off there, in the last row too; lengths within them give what a copy of the view gives."""
+    big = torch.full((5, 200 + cols), 640, dtype=torch.int32, device="cuda")   # a page that is no request's
+    view = big[:, 200:]
+    view[:] = 64 * (torch.arange(5, device="cuda")[:, None] * 9 + torch.arange(cols, device="cuda") // 64) + torch.arange(
+        cols, device="cuda") % 64
+    rpi = torch.tensor([4, 0, 2], device="cuda")
+    width, reach = 11, -(-cols // 64)
+    for lens, code in (([cols, 1, 130], 0), ([700, 700, 64], 4)):
+        sl = torch.tensor(lens, device="cuda")
+        want = [[9 * r + p if p < min(reach, -(-n // 64)) else -1 for p in range(width)] for r, n in zip([4, 0, 2], lens)]
+        assert mla.build_block_table(view, rpi, sl, width).tolist() == want and mla.read_device_error() == code
+        bt, seqlens, _, _ = mla.build_decode_metadata(view, rpi, sl, width, 16)
+        assert bt.tolist() == want and seqlens.tolist() == lens and mla.read_device_error() == code
+        kept = torch.full((3, width), 77, dtype=torch.int32, device="cuda")
+        mla.build_block_table(view, rpi, sl, width, out=kept, fill_tail=False)
+        assert kept.tolist() == [[77 if x < 0 else x for x in row] for row in want] and mla.read_device_error() == code
+    cache = torch.randn(45, 64, 576, device="cuda").bfloat16()
+    q, k_new = torch.randn(3, 2, 16, 576, device="cuda").bfloat16(), torch.randn(3, 2, 576, device="cuda").bfloat16()
+    sl = torch.tensor([cols, 1, 130], dtype=torch.int32, device="cuda")
+    got = mla.extend_paged_prefix(q, k_new, cache, view, rpi, sl, width, SCALE)
+    same = mla.extend_paged_prefix(q, k_new, cache, view.contiguous(), rpi, sl, reach, SCALE)
+    assert mla.read_device_error() == 0 and torch.equal(got[0], same[0]) and torch.equal(got[1], same[1])
+    mla.extend_paged_prefix(q, k_new, cache, view, rpi, sl + 200, width, SCALE)
+    assert mla.read_device_error() & 4
+
+
+@gpu
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("cut,width", [
