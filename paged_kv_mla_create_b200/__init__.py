@@ -595,6 +595,8 @@ def mla_chunk_paged(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.T
         raise ValueError("out must be a contiguous bf16 [num_tokens, h_q, head_dim_v] tensor")
     if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or tuple(lse.shape) != (num_tokens, h_q)):
         raise ValueError("lse must be a contiguous float32 [num_tokens, h_q] tensor")
+    if workspace is not None and not workspace.is_contiguous():   # (an expanded one has fewer bytes than elements)
+        raise ValueError("workspace must be contiguous")
     parts = int(chunk_plan.shape[0])
     with _on(dev):
         if out is None:

@@ -195,6 +195,19 @@ def test_a_plan_buffer_of_other_rows_is_refused():
     assert mla.read_device_error() == 0
 
 
+@gpu
+def test_a_workspace_that_is_not_memory_of_its_size_is_refused():
+    b = Batch([300, 70], [5, 40], seed=3)
+    bt, seqlens, cu, _, _, plan, _ = b.maps(16)
+    cache, _, _ = make_cache(b, "bf16", 1)
+    q = torch.randn(b.rows, 16, 576, device="cuda").bfloat16()
+    need = mla.chunk_workspace_bytes(mla.num_chunk_parts())
+    for ws in (torch.zeros(1, dtype=torch.uint8, device="cuda").expand(need), torch.zeros(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            mla.mla_chunk_paged(q, cache, bt, seqlens, cu, 512, plan, SCALE, workspace=ws)
+    assert mla.read_device_error() == 0
+
+
 def test_view_validation_happens_before_any_launch():
     f = mla.library().mla_build_chunk_metadata_view
     args = [1 << 20, 5, 192, 64, 1 << 21, 3, 1 << 22, 1 << 23, 2, 2, 9, None, 0, 16, 1, 74, 1 << 24, 3, 3, 64, 1, -1, 1 << 25, 1 << 26,
