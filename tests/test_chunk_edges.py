@@ -196,6 +196,76 @@ def test_a_plan_buffer_of_other_rows_is_refused():
 
 
 @gpu
+@pytest.mark.parametrize("kv", ["bf16", "e4m3", "e5m2"])
+@pytest.mark.parametrize("parts", [1, 74])
+def test_a_bad_page_reads_as_zeros(parts, kv):
+    """A page outside the pool is reported and counts as 64 rows of zeros (scores and values), wherever it lies."""
+    b = Batch([1300, 100], [5, 40], seed=3)
+    h = 16
+    bt, seqlens, cu, _, _, plan, _ = b.maps(h, num_parts=parts)
+    cache, scale, values = make_cache(b, kv, 1)
+    q = torch.randn(b.rows, h, 576, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").bfloat16()
+    for bad, pages in ((-1, [1]), (b.pool, [0, 7]), (2**31 - 1, [20]), (-2**31, [2, 3])):
+        t = bt.clone()
+        t[0, pages] = bad
+        o, lse = mla.mla_chunk_paged(q, cache, t, seqlens, cu, 512, plan, SCALE, descale_k=scale)
+        assert mla.read_device_error() == 1
+        at = 0
+        for r, n in enumerate(b.chunk):
+            keys = values[torch.tensor(b.slots[r], device="cuda")]
+            if r == 0:
+                for p in pages:
+                    keys[64 * p:64 * p + 64] = 0
+            ro, rl, pv, ds = reference(q[at:at + n], keys, True)
+            assert_attention(o[at:at + n], lse[at:at + n], ro, rl, pv, ds, b.L[r], kv, float(keys.abs().max()))
+            at += n
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["e4m3", "e5m2"])
+def test_8_bit_pages_past_four_gigabytes(kv):
+    """Byte offsets past 32 bits in an 8-bit pool, whose rows come by other loads than a bf16 one's."""
+    b = Batch([500, 70], [20, 3], seed=4)
+    shift = 120000   # pages of 36,864 bytes
+    bt, seqlens, cu, _, _, plan, _ = b.maps(16)
+    cache, scale, _ = make_cache(b, kv, 5)
+    big = torch.full((shift + b.pool, 64, 576), 0x7F, dtype=torch.uint8, device="cuda")   # NaN
+    big[shift:] = cache.view(torch.uint8)
+    q = torch.randn(b.rows, 16, 576, device="cuda").bfloat16()
+    table = torch.where(bt >= 0, bt + shift, bt)
+    o, lse = mla.mla_chunk_paged(q, big.view(cache.dtype), table, seqlens, cu, 512, plan, SCALE, descale_k=scale)
+    o2, lse2 = mla.mla_chunk_paged(q, cache, bt, seqlens, cu, 512, plan, SCALE, descale_k=scale)
+    assert mla.read_device_error() == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert bool(torch.isfinite(o).all())
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 5, 70])
+def test_agrees_with_the_extend_call(n):
+    """A uniform chunk gives what extend_paged_prefix gives.  With u, ds, pv as for the 64-bit tests, the ragged call is
+    off by (u + 2 ds) pv + 2^-8 |o|.  The extend call's two parts are off by as much each, weighted to one, with
+    |o_part| <= pv_part (so 2^-8 pv for their roundings), their weights by a relative 2 ds and 2^-18 for the
+    exponentials, and its result by 2^-8 |o|.  The extend call takes finite pools only, the ragged one any tail rows."""
+    b = Batch([1000, 63, 2500, 0], [n] * 4, seed=6)
+    h = 16
+    bt, seqlens, cu, _, _, plan, _ = b.maps(h)
+    cache, _, values = make_cache(b, "bf16", 7)
+    q = torch.randn(b.rows, h, 576, generator=torch.Generator(device="cuda").manual_seed(8), device="cuda").bfloat16()
+    o, lse = mla.mla_chunk_paged(q, cache, bt, seqlens, cu, 512, plan, SCALE)
+    new = torch.stack([cache.view(-1, 576)[torch.tensor(s[p:], device="cuda")] for s, p in zip(b.slots, b.prefix)])
+    finite = torch.nan_to_num(cache, nan=3.0)
+    o2, lse2 = mla.extend_paged_prefix(q.view(4, n, h, 576), new, finite, b.r2t, b.rpi, b.prefix_t, 40, SCALE)
+    assert mla.read_device_error() == 0
+    for r in range(4):
+        at = r * n
+        ro, rl, pv, ds = reference(q[at:at + n], values[torch.tensor(b.slots[r], device="cuda")], True)
+        u = 2.0**-8
+        tol = 2 * (u + 2 * ds) * pv + (u + 2 * ds + 2.0**-18) * pv + 2 * u * ro.abs()
+        assert bool(((o[at:at + n].double() - o2[r].double()).abs() <= tol).all())
+        assert bool(((lse[at:at + n] - lse2[r]).abs() <= 2 * (ds + b.L[r] * 2.0**-24) + 2.0**-20 * (1 + rl.abs())).all())
+
+
+@gpu
 def test_a_workspace_that_is_not_memory_of_its_size_is_refused():
     b = Batch([300, 70], [5, 40], seed=3)
     bt, seqlens, cu, _, _, plan, _ = b.maps(16)
