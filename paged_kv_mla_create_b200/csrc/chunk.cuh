@@ -61,7 +61,6 @@ using decode::kQLoChunks;
 using decode::kQWarp0;
 using decode::kRaw8Off;
 using decode::kRescaleThreshold;
-using decode::kSoftmaxWarp0;
 using decode::kTmemCols;
 using decode::kTmemO;
 using decode::kTmemQ;
@@ -122,7 +121,6 @@ static_assert(kOffBar % 8 == 0, "mbarriers are 8 bytes");
 __host__ __device__ constexpr size_t part_o_floats(int parts) { return (size_t)parts * 2 * kTileRows * kDv; }
 
 struct Params {
-    const __nv_bfloat16* q;        // [num_tokens * h, 576]
     const uint8_t* kv;             // [num_pages * 64, 576]
     const int32_t* block_table;    // [bs, bt_stride]
     int64_t bt_stride;
@@ -130,7 +128,7 @@ struct Params {
     const int32_t* cache_seqlens;  // [bs]
     const int32_t* cu;             // [bs + 1]
     const int32_t* plan;           // [parts, 8]
-    int32_t bs, h, num_tokens, parts;
+    int32_t bs, h, num_tokens;
     int64_t num_pages;
     float scale_log2;              // softmax_scale * log2(e)
     const float* descale_q;        // nullable

@@ -770,7 +770,6 @@ mla_status_t mla_chunk_paged(const void* q, int32_t q_dtype, int32_t num_tokens,
     if (!ok) return MLA_ERR_CUDA;
 
     Params p;
-    p.q = static_cast<const __nv_bfloat16*>(q);
     p.kv = static_cast<const uint8_t*>(k_cache);
     p.block_table = block_table;
     p.bt_stride = block_table_stride;
@@ -781,7 +780,6 @@ mla_status_t mla_chunk_paged(const void* q, int32_t q_dtype, int32_t num_tokens,
     p.bs = bs;
     p.h = h_q;
     p.num_tokens = num_tokens;
-    p.parts = num_parts;
     p.num_pages = num_pages;
     p.scale_log2 = softmax_scale * 1.4426950408889634f;
     p.descale_q = descale_q;
