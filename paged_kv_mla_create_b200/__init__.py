@@ -513,7 +513,7 @@ def build_chunk_metadata(req_to_token: torch.Tensor, req_pool_indices: torch.Ten
     if max(num_tokens, max_seqlen_pad, num_heads, abs(pad_slot), num_parts or 0) > 0x7FFFFFFF:
         raise ValueError("num_tokens, max_seqlen_pad, num_heads, pad_slot and num_parts must fit into 32 bits")
     bs = req_pool_indices.shape[0]
-    if not (tuple(req_pool_indices.shape) == tuple(prefix_lens.shape) == tuple(chunk_lens.shape) == (bs,)):
+    if not (req_pool_indices.shape == prefix_lens.shape == chunk_lens.shape == (bs,)):
         raise ValueError("req_pool_indices, prefix_lens and chunk_lens must be vectors of one entry per request")
     if prefix_lens.dtype != chunk_lens.dtype:
         raise ValueError("prefix_lens and chunk_lens must have the same dtype")
@@ -544,12 +544,13 @@ def build_chunk_metadata(req_to_token: torch.Tensor, req_pool_indices: torch.Ten
         if taken is not None:
             _int32_vector(taken, "pages_taken", 1)
     bt, taken = out[0], out[6]
+    map_rows, map_cols = req_to_token.shape
     # a free list without entries is still a list (its data pointer may be null)
     free_ptr = None if free_pages is None else free_pages.data_ptr() or rpi.data_ptr()
     with _on(dev):
         _check(library().mla_build_chunk_metadata_view(
-            _addr(req_to_token), req_to_token.shape[0], req_to_token.stride(0), req_to_token.shape[1], _addr(rpi),
-            _index_dtype(rpi), _addr(pl), _addr(cl), _index_dtype(pl), bs, int(num_tokens), free_ptr,
+            _addr(req_to_token), map_rows, req_to_token.stride(0), map_cols, _addr(rpi), _index_dtype(rpi), _addr(pl),
+            _addr(cl), _index_dtype(pl), bs, int(num_tokens), free_ptr,
             free_pages.shape[0] if free_pages is not None else 0, int(num_heads), int(bool(causal)), parts, _addr(bt),
             bt.stride(0), int(max_seqlen_pad), PAGE_SIZE, int(bool(fill_tail)), int(pad_slot), _addr(seqlens), _addr(cu),
             _addr(positions), _addr(loc), _addr(plan), _addr(taken), _stream(dev)), "mla_build_chunk_metadata")
