@@ -475,19 +475,19 @@ MLA_API mla_status_t mla_chunk_paged(const void* q, int32_t q_dtype, int32_t num
                                      size_t workspace_bytes, mla_stream_t stream);
 
 /*
- * Test hooks for the failure path of mla_decode_paged; not for production use.  They set
- * process-wide values that every later mla_decode_paged launch (from any thread) takes:
+ * Test hooks for the failure paths of mla_decode_paged and mla_chunk_paged; not for production use.
+ * They set process-wide values that every later launch of the two (from any thread) takes:
  *   wait_budget_ns  the budget of one pipeline wait (0 restores the default of 2 s);
  *   withhold_tile   the index (within a scheduler part, counting from 0) of a tile whose page
  *                   load the leader CTA of every pair does not issue, so that the wait for it
  *                   runs out (-1 restores normal operation);
- *   no_fold_in      nonzero: the last piece of a split request never folds the other pieces
- *                   into its own result but stores its partial and merges at the end of its
- *                   part (the two ways give identical bits; 0 restores normal operation).
+ *   no_fold_in      (mla_decode_paged) nonzero: the last piece of a split request never folds the
+ *                   other pieces into its own result but stores its partial and merges at the end
+ *                   of its part (the two ways give identical bits; 0 restores normal operation).
  * When a wait runs out the CTA records MLA_DEVERR_WAIT_TIMEOUT, both CTAs of the pair stop at
  * their next wait, let their issued copies land, release their tensor memory and return; the
- * call's outputs are then undefined and its workspace must be zero-filled again.  Host-only,
- * no synchronisation.  Returns MLA_ERR_INVALID_ARG for withhold_tile < -1.
+ * call's outputs are then undefined, and mla_decode_paged's workspace must be zero-filled again.
+ * Host-only, no synchronisation.  Returns MLA_ERR_INVALID_ARG for withhold_tile < -1.
  */
 MLA_API mla_status_t mla_set_test_hooks(uint64_t wait_budget_ns, int32_t withhold_tile, int32_t no_fold_in);
 

@@ -26,8 +26,9 @@
 //   * Rows of a page at or past L (never written) are cleared in shared memory before P V reads
 //     them: P is 0 there, but 0 x NaN is not.
 //
-// What bounds it.  A tile of 128 keys is ~2,170 cycles of MMAs; a two-slot page ring turns round in
-// load 900 + S + softmax 2,000 + PV + signals, which leaves ~3,240 cycles a tile (bf16).  At that rate
+// What bounds it.  A tile of 128 keys is ~2,170 cycles of MMAs, and 328 KB through each CTA's shared memory
+// (operands 208, pages in 104, P 16), 2,560 cycles; a two-slot page ring turns round in load 900 + S +
+// softmax 2,000 + PV + signals, which leaves ~3,240 cycles a tile (bf16).  At that rate
 // a long chunk runs into the power limit (1.44-1.72 GHz): 2,000 tokens of 128 heads at 32,768 keys take
 // 15.8 ms (calls in a row), 1.19 PFLOP/s, 84 % of a sustained library GEMM.  An 8-bit cache adds the
 // widening to every tile (~3,800 cycles, 0.83 PFLOP/s).  One token a request reads the cache once: 64
