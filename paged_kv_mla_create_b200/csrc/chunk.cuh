@@ -1017,17 +1017,16 @@ constexpr int kMergeCtasPerPart = 6;   // three CTAs an SM, all resident at once
 constexpr int kMergeMaxParts = 1024;
 
 template <int kCols, int kAhead>
-__device__ __forceinline__ void merge_unit_row(const int32_t* __restrict__ plan, int2 tk, int tiles, int row, int col0, int64_t orow,
+__device__ __forceinline__ void merge_unit_row(const int32_t* __restrict__ plan, int2 tk, int row, int col0, int64_t orow,
                                                const float* __restrict__ part_o, const float* __restrict__ part_lse,
                                                __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int lane) {
     const int pieces = tk.y + 1;
     auto slot_row = [&](int k) { return (int64_t)(k == 0 ? 2 * tk.x + 1 : 2 * (tk.x + k)) * kTileRows + row; };
     auto lse_of = [&](int k) -> float {
         if (k >= pieces) return -INFINITY;
-        if (k > 0) {   // a part that begins inside the unit but holds none of its keys
+        if (k > 0) {   // a part that begins inside the unit but holds none of it
             const int32_t* e = plan + 8 * (int64_t)(tk.x + k);
-            const int end = e[0] == e[3] && e[1] == e[4] ? min(e[5], tiles) : tiles;
-            if (e[2] >= end) return -INFINITY;
+            if (e[0] == e[3] && e[1] == e[4] && e[2] >= e[5]) return -INFINITY;
         }
         return part_lse[slot_row(k)];
     };
@@ -1084,35 +1083,29 @@ chunk_merge_kernel(const int32_t* __restrict__ plan, const int32_t* __restrict__
                    int32_t max_keys, int32_t causal, const float* __restrict__ part_o, const float* __restrict__ part_lse,
                    __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
     __shared__ int2 task[kMergeMaxParts];   // part that begins the unit, parts that continue it
-    __shared__ int task_tiles[kMergeMaxParts];   // the unit's key tiles
     __shared__ int ntask;
     const int lane = threadIdx.x & 31;
     if (threadIdx.x < 32) {   // in part order: every CTA must number the units alike
         int count = 0;
         for (int i0 = 0; i0 < parts; i0 += 32) {
             const int i = i0 + lane;
-            int n = 0, tiles = 0;
+            int n = 0;
             if (i < parts) {
                 const int32_t* r = plan + 8 * (int64_t)i;
                 const int b = r[3], m = r[4], t = r[5];
                 const bool continues = r[0] == b && r[1] == m && (r[2] > 0 || r[2] >= t);
                 if (t > 0 && b >= 0 && b < bs && m >= 0 && !continues) {
-                    for (const int32_t* e = r + 8; i + 1 + n < parts && e[0] == b && e[1] == m && e[2] > 0; e += 8) ++n;
-                }
-                if (n > 0) {
-                    int c0, rows;
+                    int c0, rows, tiles = 0;
                     request_rows(cu, b, num_tokens, c0, rows);
                     if ((int64_t)m * kTileRows < (int64_t)rows * h)
                         tiles = (table_keys(cache_seqlens[b], rows, h, m, causal, max_keys) + kTileKeys - 1) / kTileKeys;
-                    if (t >= tiles) n = 0;   // whole, or no unit at all
+                    // (t >= tiles: whole, or no unit at all; a part that begins there holds none of it)
+                    if (t < tiles)
+                        for (const int32_t* e = r + 8; i + 1 + n < parts && e[0] == b && e[1] == m && e[2] > 0 && e[2] < tiles; e += 8) ++n;
                 }
             }
             const unsigned found = __ballot_sync(0xffffffffu, n > 0);
-            if (n > 0) {
-                const int at = count + __popc(found & ((1u << lane) - 1u));
-                task[at] = make_int2(i, n);
-                task_tiles[at] = tiles;
-            }
+            if (n > 0) task[count + __popc(found & ((1u << lane) - 1u))] = make_int2(i, n);
             count += __popc(found);
         }
         if (lane == 0) ntask = count;
@@ -1127,7 +1120,6 @@ chunk_merge_kernel(const int32_t* __restrict__ plan, const int32_t* __restrict__
         const int64_t unit_row = quarters ? w >> 2 : w;
         const int row = (int)(unit_row % kTileRows);
         const int2 tk = task[unit_row / kTileRows];
-        const int tiles = task_tiles[unit_row / kTileRows];
         const int32_t* r = plan + 8 * (int64_t)tk.x;
         int c0, n;
         request_rows(cu, r[3], num_tokens, c0, n);
@@ -1135,9 +1127,9 @@ chunk_merge_kernel(const int32_t* __restrict__ plan, const int32_t* __restrict__
         if (in_req >= (int64_t)n * h) continue;
         const int64_t orow = (int64_t)c0 * h + in_req;
         if (quarters)
-            merge_unit_row<4, 8>(plan, tk, tiles, row, 128 * (int)(w & 3), orow, part_o, part_lse, out, lse, lane);
+            merge_unit_row<4, 8>(plan, tk, row, 128 * (int)(w & 3), orow, part_o, part_lse, out, lse, lane);
         else
-            merge_unit_row<16, 2>(plan, tk, tiles, row, 0, orow, part_o, part_lse, out, lse, lane);
+            merge_unit_row<16, 2>(plan, tk, row, 0, orow, part_o, part_lse, out, lse, lane);
     }
 }
 
