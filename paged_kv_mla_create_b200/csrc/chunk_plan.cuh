@@ -180,23 +180,20 @@ __device__ __forceinline__ void sum_requests(int bs, int32_t rows, MetaSmem& s) 
 template <typename IdxT, typename LenT>
 __device__ __forceinline__ void scan_requests(const MetaParams& a, MetaSmem& s) {
     const int tid = threadIdx.x;
-    for (int b = tid; b < a.bs; b += kMetaThreads) {
-        const int32_t n = (int32_t)safe_len(load_index<LenT>(a.chunk_lens, b));
-        s.cu[b + 1] = n;
-        s.off[b + 1] = new_pages<IdxT, LenT>(a, b, n);
-    }
     if (tid == 0) s.cu[0] = s.off[0] = 0;
-    sum_requests(a.bs, a.num_tokens + 1, s);   // (num_tokens < 2^31 - 256)
-    if (s.cu[a.bs] <= a.num_tokens) return;
-    for (int b = tid; b < a.bs; b += kMetaThreads)
-        s.off[b + 1] = min(s.cu[b + 1], a.num_tokens) - min(s.cu[b], a.num_tokens);
-    __syncthreads();
-    for (int b = tid; b < a.bs; b += kMetaThreads) {
-        const int32_t n = s.off[b + 1];
-        s.cu[b + 1] = n;
-        s.off[b + 1] = new_pages<IdxT, LenT>(a, b, n);
+    // (a loop of one pass, or of two: a second copy of the sums would make every launch's code longer)
+    for (bool cut = false;; cut = true) {
+        for (int b = tid; b < a.bs; b += kMetaThreads) {
+            const int32_t n = cut ? s.off[b + 1] : (int32_t)safe_len(load_index<LenT>(a.chunk_lens, b));
+            s.cu[b + 1] = n;
+            s.off[b + 1] = new_pages<IdxT, LenT>(a, b, n);
+        }
+        sum_requests(a.bs, cut ? a.num_tokens : a.num_tokens + 1, s);   // (num_tokens < 2^31 - 256)
+        if (s.cu[a.bs] <= a.num_tokens) return;
+        for (int b = tid; b < a.bs; b += kMetaThreads)
+            s.off[b + 1] = min(s.cu[b + 1], a.num_tokens) - min(s.cu[b], a.num_tokens);
+        __syncthreads();
     }
-    sum_requests(a.bs, a.num_tokens, s);
 }
 
 // Page of entry (b, p), p < total: from the free list or from req_to_token; -1 where there is none.
